@@ -390,6 +390,138 @@ bitlinear_status bitlinear_forward_relu2_glu(const bitlinear_weights* w_gate, co
 bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w, const uint16_t* x, int32_t M, uint16_t* y,
                                            int32_t* acc, uint32_t flags, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training
+ *
+ * What a training step of BitLinear layers needs beside the forward calls.
+ * The pages train through the quantisers with the straight-through estimator
+ * ("BitNet 1-Bit LLM" blog, section "BitNet b1.58: Absmean quantization
+ * function": x + (x_q - x).detach(), the weights alike), so with x~ the
+ * activation that a layer's 8-bit codes stand for and W_t its packed matrix,
+ *     dx = alpha dy W_t,       dW = dy^T x~
+ * are the gradients of the layer's input and of its latent weights.  The codes
+ * and their scales are all that the forward pass has to keep of x: they are
+ * the checkpoint of the activation, in 8 bits.
+ *
+ * Value of a code: v = RN32(q * RN32(gamma / 127)); restored as an activation
+ * (bitlinear_dequant_act, and the x~ of bitlinear_backward_weight) it is
+ * rounded once more, to bf16, the type the activation had.
+ *
+ * Rows may be strided: ld* counts elements between rows and is at least the
+ * row's length.  Rows of 16-byte aligned matrices whose ld is a multiple of 8
+ * (bf16) or 16 (codes) are read 16 bytes at a time.  Outputs are contiguous,
+ * are written whole and may not overlap inputs.  Same inputs give the same
+ * bits: no sum depends on the order in which CTAs finish.
+ * ------------------------------------------------------------------------- */
+#define BITLINEAR_FLAG_ACCUMULATE 0x40u /* bitlinear_backward_weight: add to dW instead of writing it */
+
+/* Layer norm.  Per row: s1 = sum x, s2 = sum x^2 in fp64; mean = RN32(s1 / K);
+ * var = RN32(max(0, (s2 - s1^2 / K) / K)); rstd = RN32(1 / sqrt(var + eps)) (root
+ * and quotient in fp64); xn = RN32(RN32(RN32(x - mean) * rstd) * w), then
+ * RN32(xn + b) with a bias; y = bf16 of xn.
+ * x        device, bf16 bits [M, ldx];  w, b  device, fp32 [K] (b may be NULL).
+ * eps      0 <= eps <= 1 (with eps = 0 a constant row is undefined).
+ * y        device, out: bf16 bits [M, K].
+ * mean, rstd  device, out (may be NULL): fp32 [M], for the backward pass.
+ * Errors: NULL, SHAPE (also ldx < K, eps out of range), ALIGN, DEVICE, CUDA. */
+bitlinear_status bitlinear_layernorm(const uint16_t* x, int64_t ldx, int32_t M, int32_t K, const float* w,
+                                     const float* b, float eps, uint16_t* y, float* mean, float* rstd, void* stream);
+
+/* The same xn, quantised per token as bitlinear_quant_act does (xn is not
+ * rounded to bf16 first): what a BitLinear behind a layer norm reads, and at
+ * once the 8-bit checkpoint of its input.  q int8 [M, K], gamma fp32 [M],
+ * rowsum int32 [M] (may be NULL).  Errors: as bitlinear_layernorm. */
+bitlinear_status bitlinear_layernorm_quant_act(const uint16_t* x, int64_t ldx, int32_t M, int32_t K, const float* w,
+                                               const float* b, float eps, int8_t* q, float* gamma, int32_t* rowsum,
+                                               float* mean, float* rstd, void* stream);
+
+/* Layer norm's backward pass: with xh = (x - mean) rstd and a = dy w per row
+ *   dx = rstd (a - mean_k(a) - xh mean_k(a xh)),  dw = sum_m dy xh,  db = sum_m dy,
+ * in fp32, dx rounded once to bf16.
+ * dy, x    device, bf16 bits [M, lddy], [M, ldx];  w fp32 [K];  mean, rstd fp32
+ *          [M] as the forward call wrote them.
+ * dx       device, out: bf16 bits [M, K];  dw  fp32 [K];  db  fp32 [K] (may be NULL).
+ * workspace, workspace_bytes: device scratch of at least
+ *          bitlinear_norm_backward_workspace_bytes(M, K), 16-byte aligned.
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA. */
+size_t bitlinear_norm_backward_workspace_bytes(int32_t M, int32_t K);
+bitlinear_status bitlinear_layernorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                              int32_t M, int32_t K, const float* w, const float* mean,
+                                              const float* rstd, uint16_t* dx, float* dw, float* db, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+
+/* The backward pass of the RMSNorm of bitlinear_rmsnorm_quant_act and
+ * bitlinear_forward_norm: with r = 1 / sqrt(mean_k(x^2) + eps) (recomputed),
+ * xh = x r and a = dy g
+ *   dx = r (a - xh mean_k(a xh)),  dg = sum_m dy xh.
+ * Arguments and errors as bitlinear_layernorm_backward; eps as in the forward. */
+bitlinear_status bitlinear_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                            int32_t M, int32_t K, const float* g, float eps, uint16_t* dx, float* dg,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* The activation that per-token codes stand for: y = bf16 of RN32(q * RN32(gamma / 127)).
+ * q int8 [M, ldq], gamma fp32 [M], y out bf16 bits [M, K].
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, CUDA. */
+bitlinear_status bitlinear_dequant_act(const int8_t* q, int64_t ldq, const float* gamma, int32_t M, int32_t K,
+                                       uint16_t* y, void* stream);
+
+/* The gated FFN of a training step.  From the gate's and up projection's
+ * outputs (bf16 bits [M, ldg], [M, ldu]) it forms h as
+ * bitlinear_forward_relu2_glu defines it and writes the 8-bit codes and row
+ * maxima of g, u and h, each as bitlinear_quant_act would (q_* int8 [M, N],
+ * gamma_* fp32 [M], rowsum_h int32 [M] or NULL): those of h feed
+ * bitlinear_forward_q8 of the down projection and bitlinear_backward_weight,
+ * those of g and u bitlinear_relu2_glu_backward.  h itself is not written.
+ * Errors: NULL, SHAPE (also N above BITLINEAR_MAX_K), ALIGN, DEVICE, CUDA. */
+bitlinear_status bitlinear_relu2_glu_quant_act(const uint16_t* g, int64_t ldg, const uint16_t* u, int64_t ldu,
+                                               int32_t M, int32_t N, int8_t* q_g, float* gamma_g, int8_t* q_u,
+                                               float* gamma_u, int8_t* q_h, float* gamma_h, int32_t* rowsum_h,
+                                               void* stream);
+
+/* Its backward pass from the checkpoints: with g~, u~ the values of the codes
+ * (fp32) and r = max(g~, 0),  dg = 2 dh r u~  and  du = dh r^2, in fp32, each
+ * rounded once to bf16.  dh bf16 bits [M, lddh]; dg, du out bf16 bits [M, N].
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, CUDA. */
+bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, const int8_t* q_g,
+                                              const float* gamma_g, const int8_t* q_u, const float* gamma_u, int32_t M,
+                                              int32_t N, uint16_t* dg, uint16_t* du, void* stream);
+
+/* dW = dy^T x~: the gradient of a BitLinear's latent weights from the 8-bit
+ * checkpoint of its input, x~ restored in bf16 (bitlinear_dequant_act), the
+ * products exact and the sums in fp32.  For N:M weights this is the gradient
+ * of every latent weight, kept or not (the "dual" estimator of the
+ * Sparse-BitNet review, section 3.3).
+ * dy       device, bf16 bits [M, lddy] (N used);  q  device, int8 [M, ldq] (K
+ *          used);  gamma  device, fp32 [M].
+ * dW       device, out: fp32 [N, K].
+ * workspace, workspace_bytes: device scratch of at least
+ *          bitlinear_backward_weight_workspace_bytes(M, N, K, lddy, ldq), 16-byte
+ *          aligned (may be NULL when that is 0).
+ * flags    BITLINEAR_FLAG_ACCUMULATE.
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, FLAGS, DEVICE, CUDA. */
+size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq);
+bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, const int8_t* q, int64_t ldq,
+                                           const float* gamma, int32_t M, int32_t N, int32_t K, float* dW,
+                                           void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+
+/* dx = alpha dy W_t (+ add): the gradient of a BitLinear's input, the products
+ * exact, the sums in fp32, one rounding to bf16 at the end.  add is the
+ * gradient that reaches the same input another way (the up projection's beside
+ * the gate's, or the residual path's).
+ * w        dense or N:M weights.
+ * dy       device, bf16 bits [M, lddy] (w->N used).
+ * add      device, bf16 bits [M, K], or NULL.
+ * dx       device, out: bf16 bits [M, K].
+ * workspace, workspace_bytes: device scratch of at least
+ *          bitlinear_backward_input_workspace_bytes(M, N, K, lddy, nm_n, nm_m),
+ *          16-byte aligned (may be NULL when that is 0).
+ * Errors: NULL, SHAPE, ALIGN, PATTERN, WORKSPACE, DEVICE, CUDA. */
+size_t bitlinear_backward_input_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int32_t nm_n,
+                                                int32_t nm_m);
+bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint16_t* dy, int64_t lddy, int32_t M,
+                                          const uint16_t* add, uint16_t* dx, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
 /* Synchronises stream and reads the current device's status word into *code
  * (0 = no kernel gave up on a wait).  If clear != 0 the word is reset.
  * Codes: 1 weight/activation copies, 2 weight unpacking, 3 MMA issue, 4

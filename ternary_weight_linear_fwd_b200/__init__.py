@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 __all__ = [
     "BitLinearError", "PackedWeights", "lib", "packed_layout", "pack_weights", "pack_ternary",
@@ -18,6 +18,9 @@ __all__ = [
     "forward_workspace_bytes", "device_status", "last_kernel", "layout_version", "hadamard_quant_act4",
     "forward_hbit", "HBIT_MAX_K", "forward_q8", "forward_q8_workspace_bytes", "forward_relu2_glu",
     "forward_relu2_glu_workspace_bytes",
+    "layernorm", "layernorm_quant_act", "layernorm_backward", "rmsnorm_backward", "norm_backward_workspace_bytes",
+    "dequant_act", "Relu2GluCheckpoint", "relu2_glu_quant_act", "relu2_glu_backward", "backward_weight",
+    "backward_weight_workspace_bytes", "backward_input", "backward_input_workspace_bytes", "FLAG_ACCUMULATE",
     "FLAG_PDL", "FLAG_PATH_GEMV", "FLAG_PATH_TC", "FLAG_DECODE_LUT", "FLAG_PATH_PERSISTENT", "FLAG_NM24_EXPAND",
 ]
 
@@ -28,6 +31,7 @@ FLAG_PATH_TC = 0x4
 FLAG_DECODE_LUT = 0x8
 FLAG_PATH_PERSISTENT = 0x10
 FLAG_NM24_EXPAND = 0x20
+FLAG_ACCUMULATE = 0x40
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbitlinear.so")
@@ -79,6 +83,18 @@ def lib() -> ctypes.CDLL:
             "bitlinear_forward_relu2_glu": (st, [ctypes.POINTER(_Weights), ctypes.POINTER(_Weights), P, i32, P, P, sz,
                                                  u32, P]),
             "bitlinear_forward_relu2_glu_workspace_bytes": (sz, [i32, i32, i32, u32]),
+            "bitlinear_layernorm": (st, [P, i64, i32, i32, P, P, ctypes.c_float, P, P, P, P]),
+            "bitlinear_layernorm_quant_act": (st, [P, i64, i32, i32, P, P, ctypes.c_float, P, P, P, P, P, P]),
+            "bitlinear_norm_backward_workspace_bytes": (sz, [i32, i32]),
+            "bitlinear_layernorm_backward": (st, [P, i64, P, i64, i32, i32, P, P, P, P, P, P, P, sz, P]),
+            "bitlinear_rmsnorm_backward": (st, [P, i64, P, i64, i32, i32, P, ctypes.c_float, P, P, P, sz, P]),
+            "bitlinear_dequant_act": (st, [P, i64, P, i32, i32, P, P]),
+            "bitlinear_relu2_glu_quant_act": (st, [P, i64, P, i64, i32, i32, P, P, P, P, P, P, P, P]),
+            "bitlinear_relu2_glu_backward": (st, [P, i64, P, P, P, P, i32, i32, P, P, P]),
+            "bitlinear_backward_weight_workspace_bytes": (sz, [i32, i32, i32, i64, i64]),
+            "bitlinear_backward_weight": (st, [P, i64, P, i64, P, i32, i32, i32, P, P, sz, u32, P]),
+            "bitlinear_backward_input_workspace_bytes": (sz, [i32, i32, i32, i64, i32, i32]),
+            "bitlinear_backward_input": (st, [ctypes.POINTER(_Weights), P, i64, i32, P, P, P, sz, P]),
             "bitlinear_device_status": (st, [P, ctypes.POINTER(i32), i32]),
             "bitlinear_last_kernel": (ctypes.c_char_p, []),
             "bitlinear_layout_version": (i32, []),
@@ -389,6 +405,249 @@ def forward_norm(w: PackedWeights, x, g, eps: float, want_acc: bool = False, fla
     _check(lib().bitlinear_forward_norm(ctypes.byref(ws), _ptr(x), M, _ptr(g), float(eps), _ptr(y), _ptr(acc),
                                         _ptr(workspace), ws_n, flags, _stream(stream)), "forward_norm")
     return (y, acc) if want_acc else y
+
+
+# ---------------------------------------------------------------- training
+# The calls of a training step: layer norm with its backward pass, RMSNorm's backward pass, the 8-bit
+# checkpoints (the codes themselves) with what restores or reads them, and BitLinear's two gradient products.
+# Matrices may be row-strided views (unit stride inside a row); anything else is copied first.  All tensors of
+# a call are on one device, which need not be the current one; work goes to `stream` or that device's current
+# stream, and what the call allocates belongs to the stream it runs on.
+
+def _on(device, stream):
+    """Context in which a call's outputs and workspace are allocated and its kernels are launched."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream on {stream.device} for tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _mat(t, what: str, dtype, device=None, shape=None, align: int = 1):
+    """A 2-D CUDA matrix as the kernels read it: (the tensor, its row stride).  Views with unit stride inside a
+    row and rows that do not overlap pass as they are; others (expanded, transposed, misaligned) are copied."""
+    import torch
+    if not (torch.is_tensor(t) and t.is_cuda and t.dtype == dtype and t.dim() == 2):
+        raise ValueError(f"{what}: expected a 2-D {dtype} CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: expected a tensor on {device}, got one on {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    M, K = t.shape
+    ok = (K == 1 or t.stride(1) == 1) and (M == 1 or t.stride(0) >= K) and t.data_ptr() % align == 0
+    if not ok:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t, (t.stride(0) if M > 1 else K)
+
+
+def _vec(t, what: str, n: int, device, dtype=None):
+    import torch
+    dtype = dtype or torch.float32
+    if not (torch.is_tensor(t) and t.dtype == dtype and t.device == device and tuple(t.shape) == (n,)):
+        raise ValueError(f"{what}: expected a {dtype} tensor of {n} elements on {device}")
+    return t.contiguous()
+
+
+def _scratch(workspace, need: int, device):
+    """The caller's workspace, checked, or one of the size the call needs: (tensor or None, bytes)."""
+    import torch
+    _check_workspace(workspace, device)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def layernorm(x, weight, bias=None, eps: float = 1e-5, want_stats: bool = False, out=None, stream=None):
+    """Layer norm of each row of a bf16 [M, K] matrix (weight, bias fp32 [K]): y bf16 [M, K]; with want_stats
+    (y, mean, rstd), the fp32 [M] moments that layernorm_backward takes."""
+    import torch
+    with _on(x.device, stream):
+        x, ldx = _mat(x, "x", torch.bfloat16)
+        M, K = x.shape
+        weight = _vec(weight, "weight", K, x.device)
+        bias = None if bias is None else _vec(bias, "bias", K, x.device)
+        _check_out(out, (M, K), torch.bfloat16, x.device, "out")
+        y = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        mean = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        _check(lib().bitlinear_layernorm(_ptr(x), ldx, M, K, _ptr(weight), _ptr(bias), float(eps), _ptr(y),
+                                         _ptr(mean), _ptr(rstd), _stream(stream)), "layernorm")
+    return (y, mean, rstd) if want_stats else y
+
+
+def layernorm_quant_act(x, weight, bias=None, eps: float = 1e-5, rowsum: bool = True, want_stats: bool = False,
+                        stream=None):
+    """Layer norm, then the per-token int8 codes of the result: (q, gamma, rowsum or None), with want_stats
+    also mean and rstd.  The codes feed forward_q8 and, kept, backward_weight."""
+    import torch
+    with _on(x.device, stream):
+        x, ldx = _mat(x, "x", torch.bfloat16)
+        M, K = x.shape
+        weight = _vec(weight, "weight", K, x.device)
+        bias = None if bias is None else _vec(bias, "bias", K, x.device)
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        g = torch.empty(M, dtype=torch.float32, device=x.device)
+        rs = torch.empty(M, dtype=torch.int32, device=x.device) if rowsum else None
+        mean = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        _check(lib().bitlinear_layernorm_quant_act(_ptr(x), ldx, M, K, _ptr(weight), _ptr(bias), float(eps), _ptr(q),
+                                                   _ptr(g), _ptr(rs), _ptr(mean), _ptr(rstd), _stream(stream)),
+               "layernorm_quant_act")
+    return (q, g, rs, mean, rstd) if want_stats else (q, g, rs)
+
+
+def norm_backward_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().bitlinear_norm_backward_workspace_bytes(M, K))
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, want_bias: bool = True, workspace=None, stream=None):
+    """Gradients of layernorm: (dx bf16 [M, K], dweight fp32 [K], dbias fp32 [K] or None) from the output's
+    gradient dy and the forward call's x, mean and rstd."""
+    import torch
+    with _on(x.device, stream):
+        x, ldx = _mat(x, "x", torch.bfloat16)
+        M, K = x.shape
+        dy, lddy = _mat(dy, "dy", torch.bfloat16, x.device, (M, K))
+        weight = _vec(weight, "weight", K, x.device)
+        mean, rstd = _vec(mean, "mean", M, x.device), _vec(rstd, "rstd", M, x.device)
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        dw = torch.empty(K, dtype=torch.float32, device=x.device)
+        db = torch.empty(K, dtype=torch.float32, device=x.device) if want_bias else None
+        workspace, n = _scratch(workspace, norm_backward_workspace_bytes(M, K), x.device)
+        _check(lib().bitlinear_layernorm_backward(_ptr(dy), lddy, _ptr(x), ldx, M, K, _ptr(weight), _ptr(mean),
+                                                  _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), n,
+                                                  _stream(stream)), "layernorm_backward")
+    return dx, dw, db
+
+
+def rmsnorm_backward(dy, x, g, eps: float, workspace=None, stream=None):
+    """Gradients of the RMSNorm of rmsnorm_quant_act / forward_norm: (dx bf16 [M, K], dg fp32 [K])."""
+    import torch
+    with _on(x.device, stream):
+        x, ldx = _mat(x, "x", torch.bfloat16)
+        M, K = x.shape
+        dy, lddy = _mat(dy, "dy", torch.bfloat16, x.device, (M, K))
+        g = _vec(g, "g", K, x.device)
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        dg = torch.empty(K, dtype=torch.float32, device=x.device)
+        workspace, n = _scratch(workspace, norm_backward_workspace_bytes(M, K), x.device)
+        _check(lib().bitlinear_rmsnorm_backward(_ptr(dy), lddy, _ptr(x), ldx, M, K, _ptr(g), float(eps), _ptr(dx),
+                                                _ptr(dg), _ptr(workspace), n, _stream(stream)), "rmsnorm_backward")
+    return dx, dg
+
+
+def dequant_act(q, gamma, out=None, stream=None):
+    """The activation that per-token int8 codes stand for (bf16 [M, K]): bf16 of q * gamma / 127."""
+    import torch
+    with _on(q.device, stream):
+        q, ldq = _mat(q, "q", torch.int8)
+        M, K = q.shape
+        gamma = _vec(gamma, "gamma", M, q.device)
+        _check_out(out, (M, K), torch.bfloat16, q.device, "out")
+        y = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
+        _check(lib().bitlinear_dequant_act(_ptr(q), ldq, _ptr(gamma), M, K, _ptr(y), _stream(stream)), "dequant_act")
+    return y
+
+
+class Relu2GluCheckpoint(NamedTuple):
+    """What relu2_glu_quant_act keeps: int8 codes [M, N] and fp32 row maxima [M] of the gate's output g, the up
+    projection's output u and h = RN(RN(max(g, 0)^2) * u), and the int32 row sums of h's codes."""
+    q_g: "object"
+    gamma_g: "object"
+    q_u: "object"
+    gamma_u: "object"
+    q_h: "object"
+    gamma_h: "object"
+    rowsum_h: "object"
+
+
+def relu2_glu_quant_act(g, u, stream=None) -> Relu2GluCheckpoint:
+    """The gated FFN's h in a training step, as codes for the down projection's forward_q8, with the 8-bit
+    checkpoints of g and u (bf16 [M, N], e.g. from forward_group) that relu2_glu_backward reads."""
+    import torch
+    with _on(g.device, stream):
+        g, ldg = _mat(g, "g", torch.bfloat16)
+        M, N = g.shape
+        u, ldu = _mat(u, "u", torch.bfloat16, g.device, (M, N))
+        q = [torch.empty((M, N), dtype=torch.int8, device=g.device) for _ in range(3)]
+        m = [torch.empty(M, dtype=torch.float32, device=g.device) for _ in range(3)]
+        rs = torch.empty(M, dtype=torch.int32, device=g.device)
+        _check(lib().bitlinear_relu2_glu_quant_act(_ptr(g), ldg, _ptr(u), ldu, M, N, _ptr(q[0]), _ptr(m[0]),
+                                                   _ptr(q[1]), _ptr(m[1]), _ptr(q[2]), _ptr(m[2]), _ptr(rs),
+                                                   _stream(stream)), "relu2_glu_quant_act")
+    return Relu2GluCheckpoint(q[0], m[0], q[1], m[1], q[2], m[2], rs)
+
+
+def relu2_glu_backward(dh, q_g, gamma_g, q_u, gamma_u, stream=None):
+    """Gradients of the gate's and up projection's outputs, (dg, du) bf16 [M, N], from dh and the checkpoints."""
+    import torch
+    with _on(dh.device, stream):
+        dh, lddh = _mat(dh, "dh", torch.bfloat16)
+        M, N = dh.shape
+        _check_out(q_g, (M, N), torch.int8, dh.device, "q_g")
+        _check_out(q_u, (M, N), torch.int8, dh.device, "q_u")
+        gamma_g, gamma_u = _vec(gamma_g, "gamma_g", M, dh.device), _vec(gamma_u, "gamma_u", M, dh.device)
+        dg, du = (torch.empty((M, N), dtype=torch.bfloat16, device=dh.device) for _ in range(2))
+        _check(lib().bitlinear_relu2_glu_backward(_ptr(dh), lddh, _ptr(q_g), _ptr(gamma_g), _ptr(q_u), _ptr(gamma_u),
+                                                  M, N, _ptr(dg), _ptr(du), _stream(stream)), "relu2_glu_backward")
+    return dg, du
+
+
+def backward_weight_workspace_bytes(M: int, N: int, K: int, lddy: Optional[int] = None,
+                                    ldq: Optional[int] = None) -> int:
+    return int(lib().bitlinear_backward_weight_workspace_bytes(M, N, K, N if lddy is None else lddy,
+                                                               K if ldq is None else ldq))
+
+
+def backward_weight(dy, q, gamma, out=None, accumulate: bool = False, workspace=None, stream=None):
+    """Gradient of a BitLinear's latent weights: dW = dy^T x~ (fp32 [N, K]) from the output's gradient dy (bf16
+    [M, N]) and the 8-bit checkpoint (q, gamma) of its input, as quant_act, rmsnorm_quant_act,
+    layernorm_quant_act or relu2_glu_quant_act wrote it.  accumulate: add to `out`, which is then needed."""
+    import torch
+    with _on(dy.device, stream):
+        dy, lddy = _mat(dy, "dy", torch.bfloat16, align=16)
+        M, N = dy.shape
+        q, ldq = _mat(q, "q", torch.int8, dy.device, align=16)
+        K = q.shape[1]
+        if q.shape[0] != M:
+            raise ValueError(f"backward_weight: dy has {M} rows, q has {q.shape[0]}")
+        gamma = _vec(gamma, "gamma", M, dy.device)
+        _check_out(out, (N, K), torch.float32, dy.device, "out")
+        if accumulate and out is None:
+            raise ValueError("backward_weight: accumulate needs out")
+        dW = out if out is not None else torch.empty((N, K), dtype=torch.float32, device=dy.device)
+        workspace, n = _scratch(workspace, backward_weight_workspace_bytes(M, N, K, lddy, ldq), dy.device)
+        _check(lib().bitlinear_backward_weight(_ptr(dy), lddy, _ptr(q), ldq, _ptr(gamma), M, N, K, _ptr(dW),
+                                               _ptr(workspace), n, FLAG_ACCUMULATE if accumulate else 0,
+                                               _stream(stream)), "backward_weight")
+    return dW
+
+
+def backward_input_workspace_bytes(w: PackedWeights, M: int, lddy: Optional[int] = None) -> int:
+    return int(lib().bitlinear_backward_input_workspace_bytes(M, w.N, w.K, w.N if lddy is None else lddy, w.nm_n,
+                                                              w.nm_m))
+
+
+def backward_input(w: PackedWeights, dy, add=None, out=None, workspace=None, stream=None):
+    """Gradient of a BitLinear's input: dx = alpha dy W_t (+ add), bf16 [M, K], dense or N:M weights; add is the
+    gradient that reaches the same input another way (bf16 [M, K])."""
+    import torch
+    with _on(dy.device, stream):
+        dy, lddy = _mat(dy, "dy", torch.bfloat16, align=16)
+        M = dy.shape[0]
+        if dy.shape[1] != w.N:
+            raise ValueError(f"backward_input: dy has {dy.shape[1]} columns, the weights have {w.N} rows")
+        if w.codes.device != dy.device:
+            raise ValueError(f"backward_input: weights on {w.codes.device}, dy on {dy.device}")
+        _check_out(add, (M, w.K), torch.bfloat16, dy.device, "add")
+        _check_out(out, (M, w.K), torch.bfloat16, dy.device, "out")
+        dx = out if out is not None else torch.empty((M, w.K), dtype=torch.bfloat16, device=dy.device)
+        workspace, n = _scratch(workspace, backward_input_workspace_bytes(w, M, lddy), dy.device)
+        ws = w.c_struct()
+        _check(lib().bitlinear_backward_input(ctypes.byref(ws), _ptr(dy), lddy, M, _ptr(add), _ptr(dx),
+                                              _ptr(workspace), n, _stream(stream)), "backward_input")
+    return dx
 
 
 def device_status(clear: bool = True, stream=None) -> int:

@@ -1499,6 +1499,8 @@ extern "C" bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w
   return forward_common(w, x, M, y, acc, scratch, BITLINEAR_NOALLOC_SCRATCH_BYTES, flags, stream, w->nm_m != 0);
 }
 
+#include "train_api.cuh"
+
 #ifdef BITLINEAR_TEST_HOOKS
 // ---------------------------------------------------------------- test builds only
 #include "../../include/bitlinear_test_hooks.h"

@@ -1,0 +1,389 @@
+// train_api.cuh -- the C entry points of BitLinear's training side
+// (include/bitlinear.h, section "Training"): argument checks, launch shapes and
+// launches.  Part of the library's one translation unit.
+#pragma once
+#include "train_gemm.cuh"
+
+namespace bl {
+namespace {
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+bitlinear_status check_rows(int M, int K) {
+  return M < 1 || M > BITLINEAR_MAX_M || K < 1 || K > BITLINEAR_MAX_K ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
+}
+
+// Threads a row for the element-wise kernels of 16 values a thread and step.
+int row_lanes(int K) {
+  int lanes = 32;
+  while (lanes < 256 && 16 * lanes < K) lanes *= 2;
+  return lanes;
+}
+
+// Warps a row as quant_shape picks them, at most G 16-wide groups a lane kept in registers where it fits.
+int row_warps(int M, int K, int G, int sm_count) {
+  const int groups = (K + 15) / 16;
+  int wpr = 1;
+  while (wpr < kQuantWarps && (groups > G * 32 * wpr || static_cast<int64_t>(M) * wpr < 24ll * sm_count)) wpr *= 2;
+  return wpr;
+}
+
+template <bool kCodes>
+bitlinear_status layernorm_launch(LnArgs a, cudaStream_t s, int sm_count) {
+  a.wpr = row_warps(a.M, a.K, 3, sm_count);
+  const int need = ((a.K + 15) / 16 + 32 * a.wpr - 1) / (32 * a.wpr);
+  const int rpc = kQuantWarps / a.wpr;
+  const dim3 grid((a.M + rpc - 1) / rpc), block(32 * kQuantWarps);
+  if (need <= 1) return launch(layernorm_kernel<kCodes, 1>, grid, block, 0, s, false, a);
+  if (need <= 2) return launch(layernorm_kernel<kCodes, 2>, grid, block, 0, s, false, a);
+  return launch(layernorm_kernel<kCodes, 3>, grid, block, 0, s, false, a);
+}
+
+bitlinear_status check_layernorm(const LnArgs& a) {
+  const bitlinear_status st = check_rows(a.M, a.K);
+  if (st != BITLINEAR_OK) return st;
+  if (a.ldx < a.K || !(a.eps >= 0.0f) || a.eps > 1.0f) return BITLINEAR_ERR_SHAPE;
+  if (!aligned2(a.x) || !aligned4(a.w) || !aligned4(a.b) || !aligned4(a.mean) || !aligned4(a.rstd))
+    return BITLINEAR_ERR_ALIGN;
+  return BITLINEAR_OK;
+}
+
+// Launch shape of the norm gradients: G chunks of 8 columns a thread, T threads
+// a row group, rg groups a CTA, `ctas` CTAs (partial rows of the column sums).
+// Longer rows than kNbMaxK: T = 0, `ctas` slabs of rows.
+struct NbPlan {
+  int G, T, rg, ctas;
+};
+
+NbPlan nb_plan(int M, int K, int sm_count) {
+  NbPlan p;
+  const int chunks = (K + 7) / 8;
+  if (K > kNbMaxK) {
+    p.G = p.T = p.rg = 0;
+    p.ctas = std::min(M, 64);
+    return p;
+  }
+  p.G = chunks <= kNbMaxThreads ? 1 : 2;
+  p.T = ((chunks + p.G - 1) / p.G + 31) / 32 * 32;
+  p.rg = std::max(1, std::min({kNbMaxGroups, kNbMaxThreads / p.T, (M + sm_count - 1) / sm_count}));
+  p.ctas = std::min(sm_count, (M + p.rg - 1) / p.rg);
+  return p;
+}
+
+size_t nb_part_bytes(const NbPlan& p, int K) { return align256(static_cast<size_t>(p.ctas) * 2 * K * 4); }
+
+template <bool kLayer>
+bitlinear_status norm_backward(NbArgs a, float* dw, float* db, void* ws, size_t ws_bytes, cudaStream_t s,
+                               DeviceState* dev) {
+  const NbPlan p = nb_plan(a.M, a.K, dev->sm_count);
+  const size_t part = nb_part_bytes(p, a.K);
+  if (!ws || !aligned16(ws) || ws_bytes < part + (p.T ? 0 : align256(4 * static_cast<size_t>(a.M))))
+    return BITLINEAR_ERR_WORKSPACE;
+  a.part = static_cast<float*>(ws);
+  a.T = p.T;
+  a.rg = p.rg;
+  bitlinear_status st;
+  if (p.T) {
+    const size_t smem = 4 * (static_cast<size_t>(8) * p.G * p.T + (p.rg > 1 ? a.K : 0));
+    st = p.G == 1 ? launch(norm_backward_kernel<kLayer, 1>, dim3(p.ctas), dim3(p.T * p.rg), smem, s, false, a)
+                  : launch(norm_backward_kernel<kLayer, 2>, dim3(p.ctas), dim3(p.T * p.rg), smem, s, false, a);
+  } else {
+    float* r = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part);
+    st = launch(norm_backward_long_kernel<kLayer>, dim3(a.M), dim3(1024), 0, s, false, a, r);
+    if (st != BITLINEAR_OK) return st;
+    st = launch(norm_columns_kernel<kLayer>, dim3((a.K + 255) / 256, p.ctas), dim3(256), 0, s, false, a,
+                kLayer ? a.rstd : static_cast<const float*>(r));
+  }
+  if (st != BITLINEAR_OK) return st;
+  const int64_t cols = static_cast<int64_t>(a.K) * (kLayer ? 2 : 1);
+  return launch(norm_reduce_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(1024), 0, s, true,
+                static_cast<const float*>(a.part), p.ctas, cols, static_cast<int64_t>(a.K), dw, db);
+}
+
+bitlinear_status check_norm_backward(const NbArgs& a, const float* dw, const float* db) {
+  const bitlinear_status st = check_rows(a.M, a.K);
+  if (st != BITLINEAR_OK) return st;
+  if (a.ldx < a.K || a.lddy < a.K) return BITLINEAR_ERR_SHAPE;
+  if (!aligned2(a.x) || !aligned2(a.dy) || !aligned2(a.dx) || !aligned4(a.w) || !aligned4(a.mean) ||
+      !aligned4(a.rstd) || !aligned4(dw) || !aligned4(db))
+    return BITLINEAR_ERR_ALIGN;
+  return BITLINEAR_OK;
+}
+
+}  // namespace
+}  // namespace bl
+
+using namespace bl;
+
+extern "C" {
+
+bitlinear_status bitlinear_layernorm(const uint16_t* x, int64_t ldx, int32_t M, int32_t K, const float* w,
+                                     const float* b, float eps, uint16_t* y, float* mean, float* rstd, void* stream) {
+  if (!x || !w || !y) return BITLINEAR_ERR_NULL;
+  LnArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.x = x;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.w = w;
+  a.b = b;
+  a.eps = eps;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  bitlinear_status st = check_layernorm(a);
+  if (st != BITLINEAR_OK) return st;
+  if (!aligned2(y)) return BITLINEAR_ERR_ALIGN;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  st = layernorm_launch<false>(a, static_cast<cudaStream_t>(stream), dev->sm_count);
+  if (st == BITLINEAR_OK) t_last_kernel = "layernorm";
+  return st;
+}
+
+bitlinear_status bitlinear_layernorm_quant_act(const uint16_t* x, int64_t ldx, int32_t M, int32_t K, const float* w,
+                                               const float* b, float eps, int8_t* q, float* gamma, int32_t* rowsum,
+                                               float* mean, float* rstd, void* stream) {
+  if (!x || !w || !q || !gamma) return BITLINEAR_ERR_NULL;
+  LnArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.x = x;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.w = w;
+  a.b = b;
+  a.eps = eps;
+  a.q = q;
+  a.gamma = gamma;
+  a.rowsum = rowsum;
+  a.mean = mean;
+  a.rstd = rstd;
+  bitlinear_status st = check_layernorm(a);
+  if (st != BITLINEAR_OK) return st;
+  if (!aligned4(gamma) || !aligned4(rowsum)) return BITLINEAR_ERR_ALIGN;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  st = layernorm_launch<true>(a, static_cast<cudaStream_t>(stream), dev->sm_count);
+  if (st == BITLINEAR_OK) t_last_kernel = "layernorm_quant_act";
+  return st;
+}
+
+size_t bitlinear_norm_backward_workspace_bytes(int32_t M, int32_t K) {
+  if (check_rows(M, K) != BITLINEAR_OK) return 0;
+  const NbPlan p = nb_plan(M, K, plan_sm_count());
+  return nb_part_bytes(p, K) + (p.T ? 0 : align256(4 * static_cast<size_t>(M)));
+}
+
+bitlinear_status bitlinear_layernorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                              int32_t M, int32_t K, const float* w, const float* mean,
+                                              const float* rstd, uint16_t* dx, float* dw, float* db, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  if (!dy || !x || !w || !mean || !rstd || !dx || !dw) return BITLINEAR_ERR_NULL;
+  NbArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.w = w;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = dx;
+  bitlinear_status st = check_norm_backward(a, dw, db);
+  if (st != BITLINEAR_OK) return st;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  st = norm_backward<true>(a, dw, db, workspace, workspace_bytes, static_cast<cudaStream_t>(stream), dev);
+  if (st == BITLINEAR_OK) t_last_kernel = "layernorm_backward";
+  return st;
+}
+
+bitlinear_status bitlinear_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                            int32_t M, int32_t K, const float* g, float eps, uint16_t* dx, float* dg,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dy || !x || !g || !dx || !dg) return BITLINEAR_ERR_NULL;
+  NbArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.M = M;
+  a.K = K;
+  a.w = g;
+  a.eps = eps;
+  a.dx = dx;
+  bitlinear_status st = check_norm_backward(a, dg, nullptr);
+  if (st != BITLINEAR_OK) return st;
+  if (!(eps >= 0.0f) || eps > 1.0f) return BITLINEAR_ERR_SHAPE;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  st = norm_backward<false>(a, dg, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream), dev);
+  if (st == BITLINEAR_OK) t_last_kernel = "rmsnorm_backward";
+  return st;
+}
+
+bitlinear_status bitlinear_dequant_act(const int8_t* q, int64_t ldq, const float* gamma, int32_t M, int32_t K,
+                                       uint16_t* y, void* stream) {
+  if (!q || !gamma || !y) return BITLINEAR_ERR_NULL;
+  bitlinear_status st = check_rows(M, K);
+  if (st != BITLINEAR_OK) return st;
+  if (ldq < K) return BITLINEAR_ERR_SHAPE;
+  if (!aligned4(gamma) || !aligned2(y)) return BITLINEAR_ERR_ALIGN;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  const int lanes = row_lanes(K), rpc = 256 / lanes;
+  st = launch(dequant_act_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, static_cast<cudaStream_t>(stream), false, q,
+              ldq, gamma, M, K, y, lanes);
+  if (st == BITLINEAR_OK) t_last_kernel = "dequant_act";
+  return st;
+}
+
+bitlinear_status bitlinear_relu2_glu_quant_act(const uint16_t* g, int64_t ldg, const uint16_t* u, int64_t ldu,
+                                               int32_t M, int32_t N, int8_t* q_g, float* gamma_g, int8_t* q_u,
+                                               float* gamma_u, int8_t* q_h, float* gamma_h, int32_t* rowsum_h,
+                                               void* stream) {
+  if (!g || !u || !q_g || !gamma_g || !q_u || !gamma_u || !q_h || !gamma_h) return BITLINEAR_ERR_NULL;
+  bitlinear_status st = check_rows(M, N);
+  if (st != BITLINEAR_OK) return st;
+  if (ldg < N || ldu < N) return BITLINEAR_ERR_SHAPE;
+  if (!aligned2(g) || !aligned2(u) || !aligned4(gamma_g) || !aligned4(gamma_u) || !aligned4(gamma_h) ||
+      !aligned4(rowsum_h))
+    return BITLINEAR_ERR_ALIGN;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  GluSaveArgs a;
+  a.g = g;
+  a.ldg = ldg;
+  a.u = u;
+  a.ldu = ldu;
+  a.M = M;
+  a.N = N;
+  a.qg = q_g;
+  a.qu = q_u;
+  a.qh = q_h;
+  a.gg = gamma_g;
+  a.gu = gamma_u;
+  a.gh = gamma_h;
+  a.rowsum = rowsum_h;
+  a.wpr = row_warps(M, N, 2, dev->sm_count);
+  const int need = ((N + 15) / 16 + 32 * a.wpr - 1) / (32 * a.wpr);
+  const int rpc = kQuantWarps / a.wpr;
+  const dim3 grid((M + rpc - 1) / rpc), block(32 * kQuantWarps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = need <= 1   ? launch(relu2_glu_quant_kernel<1>, grid, block, 0, s, false, a)
+       : need <= 2 ? launch(relu2_glu_quant_kernel<2>, grid, block, 0, s, false, a)
+                   : launch(relu2_glu_quant_kernel<3>, grid, block, 0, s, false, a);
+  if (st == BITLINEAR_OK) t_last_kernel = "relu2_glu_quant_act";
+  return st;
+}
+
+bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, const int8_t* q_g,
+                                              const float* gamma_g, const int8_t* q_u, const float* gamma_u, int32_t M,
+                                              int32_t N, uint16_t* dg, uint16_t* du, void* stream) {
+  if (!dh || !q_g || !gamma_g || !q_u || !gamma_u || !dg || !du) return BITLINEAR_ERR_NULL;
+  bitlinear_status st = check_rows(M, N);
+  if (st != BITLINEAR_OK) return st;
+  if (lddh < N) return BITLINEAR_ERR_SHAPE;
+  if (!aligned2(dh) || !aligned2(dg) || !aligned2(du) || !aligned4(gamma_g) || !aligned4(gamma_u))
+    return BITLINEAR_ERR_ALIGN;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  const int lanes = row_lanes(N), rpc = 256 / lanes;
+  st = launch(relu2_glu_backward_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, static_cast<cudaStream_t>(stream),
+              false, dh, lddh, q_g, gamma_g, q_u, gamma_u, M, N, dg, du, lanes);
+  if (st == BITLINEAR_OK) t_last_kernel = "relu2_glu_backward";
+  return st;
+}
+
+size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq) {
+  (void)M; (void)N; (void)K; (void)lddy; (void)ldq;
+  return 0;
+}
+
+bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, const int8_t* q, int64_t ldq,
+                                           const float* gamma, int32_t M, int32_t N, int32_t K, float* dW,
+                                           void* workspace, size_t workspace_bytes, uint32_t flags, void* stream) {
+  if (!dy || !q || !gamma || !dW) return BITLINEAR_ERR_NULL;
+  bitlinear_status st = check_nk(N, K);
+  if (st != BITLINEAR_OK) return st;
+  if (M < 1 || M > BITLINEAR_MAX_M || lddy < N || ldq < K) return BITLINEAR_ERR_SHAPE;
+  if (flags & ~static_cast<uint32_t>(BITLINEAR_FLAG_ACCUMULATE)) return BITLINEAR_ERR_FLAGS;
+  if (!aligned2(dy) || !aligned4(gamma) || !aligned4(dW)) return BITLINEAR_ERR_ALIGN;
+  (void)workspace;
+  (void)workspace_bytes;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  GradArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.q = q;
+  a.ldq = ldq;
+  a.gamma = gamma;
+  a.dw = dW;
+  a.accumulate = (flags & BITLINEAR_FLAG_ACCUMULATE) != 0;
+  st = launch(grad_plain_kernel<true>, dim3((K + 63) / 64, (N + 63) / 64), dim3(256), 0,
+              static_cast<cudaStream_t>(stream), false, a);
+  if (st == BITLINEAR_OK) t_last_kernel = "backward_weight";
+  return st;
+}
+
+size_t bitlinear_backward_input_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int32_t nm_n,
+                                                int32_t nm_m) {
+  (void)M; (void)N; (void)K; (void)lddy; (void)nm_n; (void)nm_m;
+  return 0;
+}
+
+bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint16_t* dy, int64_t lddy, int32_t M,
+                                          const uint16_t* add, uint16_t* dx, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  if (!w || !dy || !dx) return BITLINEAR_ERR_NULL;
+  bitlinear_status st = check_matrix(w, dx, nullptr);
+  if (st != BITLINEAR_OK) return st;
+  if (M < 1 || M > BITLINEAR_MAX_M || lddy < w->N) return BITLINEAR_ERR_SHAPE;
+  if (!aligned2(dy) || !aligned2(add) || !aligned2(dx)) return BITLINEAR_ERR_ALIGN;
+  (void)workspace;
+  (void)workspace_bytes;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  GradArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.M = M;
+  a.N = w->N;
+  a.K = w->K;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.codes = w->codes;
+  a.meta = w->meta;
+  st = bitlinear_packed_layout(w->N, w->K, w->nm_n, w->nm_m, &a.ldc, &a.ldm, nullptr, nullptr);
+  if (st != BITLINEAR_OK) return st;
+  a.nm_n = w->nm_n;
+  a.nm_m = w->nm_m;
+  a.alpha = w->alpha;
+  a.add = add;
+  a.dx = dx;
+  st = launch(grad_plain_kernel<false>, dim3((w->K + 63) / 64, (M + 63) / 64), dim3(256), 0,
+              static_cast<cudaStream_t>(stream), false, a);
+  if (st == BITLINEAR_OK) t_last_kernel = "backward_input";
+  return st;
+}
+
+}  // extern "C"
