@@ -408,8 +408,10 @@ bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w, const uin
  * rounded once more, to bf16, the type the activation had.
  *
  * Rows may be strided: ld* counts elements between rows and is at least the
- * row's length.  Rows of 16-byte aligned matrices whose ld is a multiple of 8
- * (bf16) or 16 (codes) are read 16 bytes at a time.  Outputs are contiguous,
+ * row's length.  Matrices whose ld is a multiple of 8 (bf16) or 16 (codes) and
+ * whose address is 16-byte aligned are read 16 bytes at a time; the two
+ * gradient products refuse (ALIGN) such an ld with another address, and copy
+ * the rows of any other ld into their workspace first.  Outputs are contiguous,
  * are written whole and may not overlap inputs.  Same inputs give the same
  * bits: no sum depends on the order in which CTAs finish.
  * ------------------------------------------------------------------------- */
@@ -495,7 +497,7 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
  *          used);  gamma  device, fp32 [M].
  * dW       device, out: fp32 [N, K].
  * workspace, workspace_bytes: device scratch of at least
- *          bitlinear_backward_weight_workspace_bytes(M, N, K, lddy, ldq), 16-byte
+ *          bitlinear_backward_weight_workspace_bytes(M, N, K, lddy, ldq), 32-byte
  *          aligned (may be NULL when that is 0).
  * flags    BITLINEAR_FLAG_ACCUMULATE.
  * Errors: NULL, SHAPE, ALIGN, WORKSPACE, FLAGS, DEVICE, CUDA. */
@@ -514,7 +516,7 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
  * dx       device, out: bf16 bits [M, K].
  * workspace, workspace_bytes: device scratch of at least
  *          bitlinear_backward_input_workspace_bytes(M, N, K, lddy, nm_n, nm_m),
- *          16-byte aligned (may be NULL when that is 0).
+ *          32-byte aligned (may be NULL when that is 0).
  * Errors: NULL, SHAPE, ALIGN, PATTERN, WORKSPACE, DEVICE, CUDA. */
 size_t bitlinear_backward_input_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int32_t nm_n,
                                                 int32_t nm_m);

@@ -297,6 +297,19 @@ __device__ __forceinline__ uint4 ldg_stream_v4(const void* p) {
   return v;
 }
 
+// 32-byte store (32-byte aligned): a whole sector a thread.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t* r) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+
 // d = c + sum_i a.u8[i] * b.s8[i]
 __device__ __forceinline__ int32_t dp4a_us(uint32_t a, uint32_t b, int32_t c) {
   int32_t d;
@@ -390,6 +403,15 @@ __device__ __forceinline__ void tc_mma_sp_i8_ss_pair(uint32_t d_tmem, uint64_t a
       "l"(a_desc), "l"(b_desc), "r"(e_tmem), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T over the pair, kind::f16 (bf16 operands, fp32 sums, M = 256).
+__device__ __forceinline__ void tc_mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Arrives once on the mbarrier at the same shared-memory offset in every CTA of
 // cta_mask when the pair MMAs issued so far by this thread complete.
 __device__ __forceinline__ void tc_commit_pair_mc(uint64_t* bar, uint16_t cta_mask) {
@@ -476,6 +498,31 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_kmajor(uint32_t smem_addr) {
   d |= static_cast<uint64_t>(1u) << 46;                    // descriptor version (sm_100)
   d |= static_cast<uint64_t>(2u) << 61;                    // swizzle mode: 128 B
   return d;
+}
+
+// The same for an operand whose M or N dimension is the contiguous one: lines
+// of 128 bytes (64 bf16) per step of K, 8-line atoms of 1024 bytes, written with
+// the 128-byte swizzle; the next 64 of M / N start block_bytes further on.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mnmajor(uint32_t smem_addr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);   // start address
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;       // leading byte offset: the next 64 of M / N
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;             // stride byte offset: the next 8 of K
+  d |= static_cast<uint64_t>(1u) << 46;                     // descriptor version (sm_100)
+  d |= static_cast<uint64_t>(2u) << 61;                     // swizzle mode: 128 B
+  return d;
+}
+
+// Instruction descriptor for kind::f16: D fp32, A and B bf16, each K-major or
+// (mn_a, mn_b) with M / N contiguous.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool mn_a, bool mn_b) {
+  return (1u << 4)                                   // D format: fp32
+         | (1u << 7)                                 // A: bf16
+         | (1u << 10)                                // B: bf16
+         | (static_cast<uint32_t>(mn_a) << 15)       // A: M contiguous
+         | (static_cast<uint32_t>(mn_b) << 16)       // B: N contiguous
+         | (static_cast<uint32_t>(n >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(m >> 4) << 24);    // M / 16
 }
 
 // Instruction descriptor for kind::i8: D s32, A u8, B s8, both K-major.

@@ -111,6 +111,107 @@ bitlinear_status check_norm_backward(const NbArgs& a, const float* dw, const flo
   return BITLINEAR_OK;
 }
 
+// ---------------------------------------------------------------- gradient products
+// How a product's 256 x 256 tiles are given to the pairs: whole rounds of
+// tiles over their whole reduction, the tiles left over cut into `split` parts.
+struct GgPlan {
+  int row_tiles, col_tiles, kblocks, full, split, per, units, pairs;
+};
+
+// Parts of the tiles left over: the fewest (rounds of pairs) x (k-blocks of a
+// part), against the cost of the slabs.  In k-blocks of 0.3 us: a part's fp32
+// tile is written in about 4 and read back by the last launch (about 10 for
+// the launch, and 1/4 per part for its bytes).
+GgPlan gg_plan(int64_t rows, int cols, int red, int sm_count) {
+  GgPlan p;
+  p.pairs = sm_count / 2;
+  p.row_tiles = static_cast<int>((rows + kGgRows - 1) / kGgRows);
+  p.col_tiles = (cols + kGgCols - 1) / kGgCols;
+  p.kblocks = (red + kGgRed - 1) / kGgRed;
+  const int tiles = p.row_tiles * p.col_tiles;  // at most 2^16 * 2^8
+  const int left = tiles % p.pairs;
+  p.full = tiles - left;
+  p.split = 1;
+  p.per = p.kblocks;
+  if (left > 0) {
+    int64_t best = 4ll * p.kblocks;
+    for (int s = 2; s <= 32 && 2 * s <= p.kblocks; ++s) {
+      const int per = (p.kblocks + s - 1) / s;
+      const int parts = (p.kblocks + per - 1) / per;
+      const int64_t rounds = (static_cast<int64_t>(left) * parts + p.pairs - 1) / p.pairs;
+      const int64_t cost = 4 * rounds * (per + 4) + 40 + static_cast<int64_t>(left) * parts / 4;
+      if (cost < best) {
+        best = cost;
+        p.split = parts;
+        p.per = per;
+      }
+    }
+  }
+  if (p.split == 1) p.full = tiles;
+  p.units = p.full + (tiles - p.full) * p.split;
+  p.pairs = std::min(p.pairs, p.units);
+  return p;
+}
+
+size_t gg_slab_bytes(const GgPlan& p) {
+  return static_cast<size_t>(p.units - p.full) * kGgSlab * 4;
+}
+
+// Workspace: slabs | dy with padded rows | codes with padded rows or expanded N:M weights.
+struct GgLayout {
+  size_t dy, b, total;  // offsets of the second and third part, whole size
+  int64_t lddy;         // row stride of dy that TMA reads, in elements
+};
+GgLayout gg_layout(const GgPlan& p, int64_t M, int64_t N, int64_t lddy, size_t b_bytes) {
+  GgLayout l;
+  l.dy = align256(gg_slab_bytes(p));
+  const bool pad = lddy % 8 != 0;
+  l.lddy = pad ? (N + 7) / 8 * 8 : lddy;
+  l.b = l.dy + (pad ? align256(static_cast<size_t>(M) * l.lddy * 2) : 0);
+  l.total = l.b + align256(b_bytes);
+  return l;
+}
+
+// Puts dy's rows where TMA can step them, if they are not.
+bitlinear_status gg_dy(const uint16_t** dy, int64_t lddy, int M, int N, uint8_t* ws, const GgLayout& l,
+                       cudaStream_t s, int sm_count) {
+  if (l.lddy == lddy) return BITLINEAR_OK;
+  uint16_t* d = reinterpret_cast<uint16_t*>(ws + l.dy);
+  const bitlinear_status st = launch(pad_rows_kernel<uint16_t>, dim3(std::min(M, 16 * sm_count)), dim3(256), 0, s, false,
+                                     *dy, lddy, static_cast<int64_t>(M), N, d, l.lddy);
+  *dy = d;
+  return st;
+}
+
+template <bool kWeight>
+bitlinear_status gg_launch(const CUtensorMap& mA, const CUtensorMap& mB, const GradArgs& a, const GgPlan& p,
+                           cudaStream_t s) {
+  bitlinear_status st = launch_ex(grad_gemm_kernel<kWeight>, dim3(2 * p.pairs), dim3(kGgThreads), GG<kWeight>::SMEM, s,
+                                  true, 2, mA, mB, a);
+  if (st != BITLINEAR_OK || p.units == p.full) return st;
+  const int tiles = p.row_tiles * p.col_tiles - p.full;
+  return launch(grad_reduce_kernel<kWeight>, dim3(8 * tiles), dim3(256), 0, s, true, a);
+}
+
+void gg_args(GradArgs* a, const GgPlan& p, int rows, int cols, int red, void* ws, DeviceState* dev) {
+  std::memset(a, 0, sizeof *a);
+  a->rows = rows;
+  a->cols = cols;
+  a->red = red;
+  a->col_tiles = p.col_tiles;
+  a->kblocks = p.kblocks;
+  a->full = p.full;
+  a->units = p.units;
+  a->split = p.split;
+  a->per = p.per;
+  a->slab = static_cast<float*>(ws);
+  a->status = dev->status;
+}
+
+size_t bw_codes_bytes(int64_t M, int K, int64_t ldq) { return ldq % 16 ? static_cast<size_t>(M) * k16(K) : 0; }
+size_t bi_codes_bytes(int N, int K, int nm_m) { return nm_m ? static_cast<size_t>(N) * dense_ld(K) : 0; }
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 }  // namespace
 }  // namespace bl
 
@@ -309,8 +410,8 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
 }
 
 size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq) {
-  (void)M; (void)N; (void)K; (void)lddy; (void)ldq;
-  return 0;
+  if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || ldq < K) return 0;
+  return gg_layout(gg_plan(N, K, M, plan_sm_count()), M, N, lddy, bw_codes_bytes(M, K, ldq)).total;
 }
 
 bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, const int8_t* q, int64_t ldq,
@@ -321,34 +422,46 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   if (st != BITLINEAR_OK) return st;
   if (M < 1 || M > BITLINEAR_MAX_M || lddy < N || ldq < K) return BITLINEAR_ERR_SHAPE;
   if (flags & ~static_cast<uint32_t>(BITLINEAR_FLAG_ACCUMULATE)) return BITLINEAR_ERR_FLAGS;
-  if (!aligned2(dy) || !aligned4(gamma) || !aligned4(dW)) return BITLINEAR_ERR_ALIGN;
-  (void)workspace;
-  (void)workspace_bytes;
+  if ((lddy % 8 ? !aligned2(dy) : !aligned16(dy)) || (ldq % 16 == 0 && !aligned16(q)) || !aligned4(gamma) ||
+      !aligned4(dW))
+    return BITLINEAR_ERR_ALIGN;
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const GgPlan p = gg_plan(N, K, M, dev->sm_count);
+  const GgLayout l = gg_layout(p, M, N, lddy, bw_codes_bytes(M, K, ldq));
+  if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);
+  if (st != BITLINEAR_OK) return st;
+  if (ldq % 16) {
+    int8_t* d = reinterpret_cast<int8_t*>(ws + l.b);
+    st = launch(pad_rows_kernel<int8_t>, dim3(std::min(M, 16 * dev->sm_count)), dim3(256), 0, s, true, q, ldq,
+                static_cast<int64_t>(M), K, d, k16(K));
+    if (st != BITLINEAR_OK) return st;
+    q = d;
+    ldq = k16(K);
+  }
+  CUtensorMap mA, mB;
+  if (!make_map_u8(&mA, dy, 2 * static_cast<uint64_t>(N), M, 2 * static_cast<uint64_t>(l.lddy), 128, kGgRed, 128) ||
+      !make_map_u8(&mB, q, K, M, static_cast<uint64_t>(ldq), 128, kGgRed, 0))
+    return BITLINEAR_ERR_CUDA;
   GradArgs a;
-  std::memset(&a, 0, sizeof a);
-  a.M = M;
-  a.N = N;
-  a.K = K;
-  a.dy = dy;
-  a.lddy = lddy;
-  a.q = q;
-  a.ldq = ldq;
+  gg_args(&a, p, N, K, M, workspace, dev);
   a.gamma = gamma;
   a.dw = dW;
   a.accumulate = (flags & BITLINEAR_FLAG_ACCUMULATE) != 0;
-  st = launch(grad_plain_kernel<true>, dim3((K + 63) / 64, (N + 63) / 64), dim3(256), 0,
-              static_cast<cudaStream_t>(stream), false, a);
+  a.vec = K % 8 == 0 && aligned32(dW);
+  st = gg_launch<true>(mA, mB, a, p, s);
   if (st == BITLINEAR_OK) t_last_kernel = "backward_weight";
   return st;
 }
 
 size_t bitlinear_backward_input_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int32_t nm_n,
                                                 int32_t nm_m) {
-  (void)M; (void)N; (void)K; (void)lddy; (void)nm_n; (void)nm_m;
-  return 0;
+  if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || !pattern_ok(nm_n, nm_m)) return 0;
+  return gg_layout(gg_plan(M, K, N, plan_sm_count()), M, N, lddy, bi_codes_bytes(N, K, nm_m)).total;
 }
 
 bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint16_t* dy, int64_t lddy, int32_t M,
@@ -357,31 +470,49 @@ bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint
   if (!w || !dy || !dx) return BITLINEAR_ERR_NULL;
   bitlinear_status st = check_matrix(w, dx, nullptr);
   if (st != BITLINEAR_OK) return st;
-  if (M < 1 || M > BITLINEAR_MAX_M || lddy < w->N) return BITLINEAR_ERR_SHAPE;
-  if (!aligned2(dy) || !aligned2(add) || !aligned2(dx)) return BITLINEAR_ERR_ALIGN;
-  (void)workspace;
-  (void)workspace_bytes;
+  const int N = w->N, K = w->K;
+  if (M < 1 || M > BITLINEAR_MAX_M || lddy < N) return BITLINEAR_ERR_SHAPE;
+  if ((lddy % 8 ? !aligned2(dy) : !aligned16(dy)) || !aligned2(add)) return BITLINEAR_ERR_ALIGN;
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
-  GradArgs a;
-  std::memset(&a, 0, sizeof a);
-  a.M = M;
-  a.N = w->N;
-  a.K = w->K;
-  a.dy = dy;
-  a.lddy = lddy;
-  a.codes = w->codes;
-  a.meta = w->meta;
-  st = bitlinear_packed_layout(w->N, w->K, w->nm_n, w->nm_m, &a.ldc, &a.ldm, nullptr, nullptr);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const GgPlan p = gg_plan(M, K, N, dev->sm_count);
+  const GgLayout l = gg_layout(p, M, N, lddy, bi_codes_bytes(N, K, w->nm_m));
+  if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);
   if (st != BITLINEAR_OK) return st;
-  a.nm_n = w->nm_n;
-  a.nm_m = w->nm_m;
+  const int64_t ld = dense_ld(K);
+  const uint8_t* codes = w->codes;
+  if (w->nm_m) {
+    NmExpandArgs e;
+    e.codes = w->codes;
+    e.meta = w->meta;
+    st = bitlinear_packed_layout(N, K, w->nm_n, w->nm_m, &e.ldc, &e.ldm, nullptr, nullptr);
+    if (st != BITLINEAR_OK) return st;
+    e.ldd = ld;
+    e.N = N;
+    e.K = K;
+    e.nm_n = w->nm_n;
+    e.nm_m = w->nm_m;
+    e.out = reinterpret_cast<uint32_t*>(ws + l.b);
+    const int64_t words = static_cast<int64_t>(N) * (ld / 4);
+    st = launch(nm_expand_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, true, e);
+    if (st != BITLINEAR_OK) return st;
+    codes = ws + l.b;
+  }
+  CUtensorMap mA, mB;
+  if (!make_map_u8(&mA, dy, 2 * static_cast<uint64_t>(N), M, 2 * static_cast<uint64_t>(l.lddy), 128, 128, 128) ||
+      !make_map_u8(&mB, codes, static_cast<uint64_t>(ld), N, static_cast<uint64_t>(ld), 32, kGgRed, 0))
+    return BITLINEAR_ERR_CUDA;
+  GradArgs a;
+  gg_args(&a, p, M, K, N, workspace, dev);
   a.alpha = w->alpha;
   a.add = add;
   a.dx = dx;
-  st = launch(grad_plain_kernel<false>, dim3((w->K + 63) / 64, (M + 63) / 64), dim3(256), 0,
-              static_cast<cudaStream_t>(stream), false, a);
+  a.vec = K % 16 == 0 && aligned32(dx) && aligned32(add);
+  st = gg_launch<false>(mA, mB, a, p, s);
   if (st == BITLINEAR_OK) t_last_kernel = "backward_input";
   return st;
 }

@@ -3,112 +3,495 @@
 // stand for, W_t the packed ternary matrix:
 //   dx = alpha dy W_t            [M, K]   (backward_input)
 //   dW = dy^T x~                 [N, K]   (backward_weight)
+//
+// Both contract dy (bf16) with an operand that lies compressed in memory with
+// the OUTPUT columns contiguous: rows of 2-bit codes (W_t, one per output
+// feature n) or of 8-bit codes (x~, one per token m).  On the tensor cores:
+//
+//   D[256 rows, 256 cols] (fp32, TMEM) += A * B over the reduction, where
+//   A = dy.  dx: rows are tokens, the reduction (n) contiguous (K-major);
+//       dW: rows are features n, contiguous, the reduction is the tokens.
+//   B = the compressed rows expanded to bf16 in shared memory, one 128-byte
+//       line per step of the reduction and 64 columns (N-contiguous operand),
+//       exactly where the packed row's codes already stand side by side, so
+//       that nothing is transposed.
+// W_t's values and the 8-bit codes are exact in bf16, dy is bf16: every product
+// is exact and the sums are fp32.  x~ = RNb(RN(q RN(gamma / 127))) carries the
+// token's scale, which cannot leave the sum over tokens; that rounding to bf16
+// is the restored activation's own type (dequant_act gives the same values).
+//
+// Two CTAs of a cluster share one MMA of 256 x 256 x 16 (cta_group::2): each
+// holds its own 128 rows of A and expands its own 128 columns of B, so each
+// column is expanded once per 256 rows and the shared-memory reads per MMA
+// halve.  Rings as in gemm_tc2.cuh: S copy stages of 64 steps of the reduction
+// (A's tile by TMA, the compressed rows), R operand slots (expanded B).  Roles:
+// warp 0 copies, warp 1 (rank 0) issues the MMAs, warp 2 owns TMEM, warps 4 ..
+// 11 expand (two groups, alternate stages), warps 12 .. 15 store.
+//
+// Persistent: one pair per two SMs walks a static list of units.  The tiles
+// that fill whole rounds of pairs run over their whole reduction; the rest are
+// cut into `split` parts of the reduction, each part's fp32 tile goes to a slab
+// of the workspace, and grad_reduce_kernel adds the parts in order and
+// finishes the tile: no atomics, the same bits every time.
 #pragma once
 #include "train_rows.cuh"
 
 namespace bl {
 
+constexpr int kGgRows = 256;      // rows of a pair tile (128 a CTA)
+constexpr int kGgCols = 256;      // columns of a pair tile (128 of B a CTA)
+constexpr int kGgRed = 64;        // steps of the reduction per stage
+constexpr int kGgThreads = 512;
+constexpr int kGgSlab = kGgRows * kGgCols;  // fp32 of one part of a split tile
+
 struct GradArgs {
-  int M, N, K;
-  const uint16_t* dy;  // bf16 [M, lddy]
-  int64_t lddy;
-  // backward_input
-  const uint8_t* codes;
-  const uint8_t* meta;
-  int64_t ldc, ldm;
-  int nm_n, nm_m;
-  const float* alpha;
-  const uint16_t* add;  // bf16 [M, K] or null
-  uint16_t* dx;         // bf16 [M, K]
-  // backward_weight
-  const int8_t* q;      // [M, ldq]
-  int64_t ldq;
-  const float* gamma;
-  float* dw;            // [N, K]
-  int accumulate;
+  int rows, cols, red;    // output rows and columns, length of the reduction
+  int col_tiles;          // tiles: column tile fastest
+  int kblocks;            // ceil(red / kGgRed)
+  int full;               // tiles run over the whole reduction; the others in `split` parts of `per` k-blocks
+  int units;              // full + (tiles - full) * split
+  int split, per;
+  const float* alpha;     // dx
+  const uint16_t* add;    // dx: bf16 [rows, cols] or null
+  uint16_t* dx;           // dx: bf16 [rows, cols]
+  const float* gamma;     // dW: [red]
+  float* dw;              // dW: fp32 [rows, cols]
+  int accumulate;         // dW: add to it
+  int vec;                // output (and add) rows are 32-byte aligned
+  float* slab;            // [(tiles - full) * split][256][256]
+  int32_t* status;
 };
 
-// One weight of a packed matrix, any pattern.
-__device__ __forceinline__ float packed_weight(const GradArgs& a, int n, int k) {
-  const uint8_t* c = a.codes + static_cast<int64_t>(n) * a.ldc;
-  int pos = k;
-  if (a.nm_m == 4) {
-    const int b = k >> 2;
-    const uint32_t nib = (a.meta[static_cast<int64_t>(n) * a.ldm + (b >> 1)] >> (4 * (b & 1))) & 15u;
-    const uint32_t j = k & 3;
-    if ((nib & 3u) == j)
-      pos = 2 * b;
-    else if ((nib >> 2) == j)
-      pos = 2 * b + 1;
-    else
-      return 0.0f;
-  } else if (a.nm_m == 8) {
-    const uint32_t mask = a.meta[static_cast<int64_t>(n) * a.ldm + (k >> 3)], j = k & 7;
-    if (!((mask >> j) & 1u)) return 0.0f;
-    pos = (k >> 3) * a.nm_n + __popc(mask & ((1u << j) - 1u));
+template <bool kWeight>
+struct GG {
+  static constexpr int A_STAGE = 128 * kGgRed * 2;               // 16 KB
+  static constexpr int RAW = kWeight ? kGgRed * 128 : kGgRed * 32;  // compressed rows: 128 codes, 1 or 1/4 byte each
+  static constexpr int OP = 128 * kGgRed * 2;                    // 16 KB of expanded B
+  static constexpr int S = kWeight ? 6 : 8;                      // even, like R: see gemm_tc2.cuh
+  static constexpr int R = 4;
+  static constexpr int FIXED = 512;
+  static constexpr int SMEM = S * (A_STAGE + RAW) + R * OP + FIXED;
+  static constexpr uint32_t IDESC = idesc_bf16(kGgRows, kGgCols, kWeight, true);
+  static_assert(SMEM <= kTcSmemMax, "shared memory");
+  static_assert(RAW % 1024 == 0, "stages keep the swizzle's alignment");
+};
+
+// 16 ternary codes (2 bits each, k from bit 0) as bf16 weights: word i holds
+// those of k = i (low half) and k = i + 8.  A code c at bit 2 j (j = 0, 1, 2) of
+// a half-word, ORed into the bf16 128, is 128 + 4^j c; one fused multiply-add
+// by 4^-j and -(128 4^-j + 1) leaves c - 1, exactly.
+__device__ __forceinline__ void ternary16_bf16(uint32_t w, uint32_t (&o)[8]) {
+  const uint32_t t[3] = {w, w >> 6, w >> 12};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int j = i % 3;
+    const uint32_t mask = 0x00030003u << (2 * j);
+    const uint32_t v = (t[i / 3] & mask) | 0x43004300u;
+    const float mul = j == 0 ? 1.0f : j == 1 ? 0.25f : 0.0625f;
+    const __nv_bfloat162 m = __floats2bfloat162_rn(mul, mul);
+    const __nv_bfloat162 s = __floats2bfloat162_rn(-(128.0f * mul + 1.0f), -(128.0f * mul + 1.0f));
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v), m, s);
+    o[i] = *reinterpret_cast<const uint32_t*>(&r);
   }
-  return static_cast<float>(static_cast<int>((c[pos >> 2] >> (2 * (pos & 3))) & 3u) - 1);
 }
 
-// Plain tiles of 64 x 64 outputs, 16 of the reduction a step, 4 x 4 outputs a
-// thread, fp32.
+// Stores one thread's 32 consecutive columns (from col) of output row `row`,
+// fp32 sums v in natural column order.
 template <bool kWeight>
-__global__ void __launch_bounds__(256) grad_plain_kernel(const GradArgs a) {
-  __shared__ float sA[16][65], sB[16][65];
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const int rows = kWeight ? a.N : a.M, cols = a.K, red = kWeight ? a.M : a.N;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int d0 = 0; d0 < red; d0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      {
-        const int d = kWeight ? i >> 6 : i & 15, r = kWeight ? i & 63 : i >> 4;
-        float v = 0.0f;
-        if (d0 + d < red && r0 + r < rows) {
-          const int64_t m = kWeight ? d0 + d : r0 + r, n = kWeight ? r0 + r : d0 + d;
-          v = bf16_bits_to_f32(a.dy[m * a.lddy + n]);
+__device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int col, const float (&v)[32],
+                                             float alpha) {
+  const int64_t at = row * a.cols + col;
+  const bool whole = a.vec && col + 32 <= a.cols;
+  if (kWeight) {
+    float* p = a.dw + at;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        uint32_t o[8];
+        if (a.accumulate) {
+          ld_global_v8(p + i, o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__fadd_rn(__uint_as_float(o[e]), v[i + e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(v[i + e]);
         }
-        sA[d][r] = v;
+        st_global_v8(p + i, o);
       }
-      {
-        const int d = i >> 6, c = i & 63;
-        float v = 0.0f;
-        if (d0 + d < red && c0 + c < cols) {
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < a.cols) p[i] = a.accumulate ? __fadd_rn(p[i], v[i]) : v[i];
+    }
+  } else {
+    uint16_t* p = a.dx + at;
+    const uint16_t* q = a.add ? a.add + at : nullptr;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
+        uint32_t o[8], s[8];
+        if (q) ld_global_v8(q + i, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float lo = __fmul_rn(v[i + 2 * e], alpha), hi = __fmul_rn(v[i + 2 * e + 1], alpha);
+          if (q) {
+            lo = __fadd_rn(lo, bf16_lo(s[e]));
+            hi = __fadd_rn(hi, bf16_hi(s[e]));
+          }
+          o[e] = pack_bf16x2(lo, hi);
+        }
+        st_global_v8(p + i, o);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < a.cols) {
+          float f = __fmul_rn(v[i], alpha);
+          if (q) f = __fadd_rn(f, bf16_bits_to_f32(q[i]));
+          p[i] = static_cast<uint16_t>(pack_bf16x2(f, 0.0f));
+        }
+    }
+  }
+}
+
+// mapA: dy; box 128 bytes x 128 rows (dx) or 128 bytes x 64 rows (dW), landed 128-byte-swizzled.
+// mapB: the compressed rows; box 32 bytes (2-bit) or 128 bytes (8-bit) x 64 rows, landed as they are.
+template <bool kWeight>
+__global__ void __launch_bounds__(kGgThreads, 1)
+    grad_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                     const GradArgs a) {
+  using C = GG<kWeight>;
+  constexpr int S = C::S, R = C::R;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // both CTAs see the same offset, so both leave here together (before any cluster barrier)
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) *a.status = kDevBadSmemAlign;
+    return;
+  }
+  uint8_t* sA = smem_raw;                   // [S][16 KB]
+  uint8_t* sOp = sA + S * C::A_STAGE;       // [R][2 blocks of 64 columns][64 lines][128 B]
+  uint8_t* sRaw = sOp + R * C::OP;          // [S][RAW]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + S * C::RAW);
+  uint64_t* empty = full + S;
+  uint64_t* opready = empty + S;     // [R] rank 0's: both CTAs' expanding warps
+  uint64_t* accfull = opready + R;   // [2]
+  uint64_t* accempty = accfull + 2;  // [2] rank 0's: both CTAs' storing warps
+  uint64_t* drain = accempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  // unit g -> its tile's first row and column, first k-block and number of k-blocks
+  auto unit_of = [&](int g, int& row0, int& col0, int& kb0) {
+    int tile = g, n = a.kblocks;
+    kb0 = 0;
+    if (g >= a.full) {
+      const int h = g - a.full;
+      tile = a.full + h / a.split;
+      kb0 = (h - (tile - a.full) * a.split) * a.per;
+      n = min(a.per, a.kblocks - kb0);
+    }
+    const int rt = tile / a.col_tiles;
+    row0 = rt * kGgRows;
+    col0 = (tile - rt * a.col_tiles) * kGgCols;
+    return n;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int j = 0; j < R; ++j) mbar_init(&opready[j], 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], 8);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&mapA);
+    tma_prefetch_desc(&mapB);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers exist before any remote arrive or multicast commit
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t opready0 = mapa_shared(smem_u32(opready), 0);
+  const uint32_t accempty0 = mapa_shared(smem_u32(accempty), 0);
+  pdl_wait_primary();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ copies (both CTAs)
+      bool ok = true;
+      int i = 0;
+      for (int g = pair; g < a.units && ok; g += npairs) {
+        int row0, col0, kb0;
+        const int n = unit_of(g, row0, col0, kb0);
+        row0 += static_cast<int>(rank) * 128;
+        col0 += static_cast<int>(rank) * 128;
+        for (int kb = kb0; kb < kb0 + n; ++kb, ++i) {
+          const int s = i % S;
+          if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1)) {
+            *a.status = kDevTimeoutProducer;
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], C::A_STAGE + C::RAW);
+          uint8_t* dA = sA + s * C::A_STAGE;
           if (kWeight) {
-            const int64_t m = d0 + d;
-            v = __fmul_rn(static_cast<float>(a.q[m * a.ldq + c0 + c]), __fdiv_rn(a.gamma[m], kQb));
-            v = __bfloat162float(__float2bfloat16_rn(v));
+            tma_load_2d(dA, &mapA, 2 * row0, kb * kGgRed, &full[s]);
+            tma_load_2d(dA + 8192, &mapA, 2 * row0 + 128, kb * kGgRed, &full[s]);
+            tma_load_2d(sRaw + s * C::RAW, &mapB, col0, kb * kGgRed, &full[s]);
           } else {
-            v = packed_weight(a, d0 + d, c0 + c);
+            tma_load_2d(dA, &mapA, kb * kGgRed * 2, row0, &full[s]);
+            tma_load_2d(sRaw + s * C::RAW, &mapB, col0 / 4, kb * kGgRed, &full[s]);
           }
         }
-        sB[d][c] = v;
+      }
+      if (!ok) {  // copies in flight land before the CTA may leave
+        for (int j = (i - S > 0 ? i - S : 0); j < i; ++j)
+          if (!mbar_wait(&full[j % S], (j / S) & 1)) *a.status = kDevTimeoutDrain;
       }
     }
-    __syncthreads();
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // ------------------------------------------------------------ MMAs (rank 0 only)
+      bool issued = false, ok = true;
+      int i = 0, t = 0;
+      for (int g = pair; g < a.units && ok; g += npairs, ++t) {
+        int row0, col0, kb0;
+        const int n = unit_of(g, row0, col0, kb0);
+        const int buf = t & 1;
+        if (t >= 2 && !mbar_wait_cluster(&accempty[buf], ((t >> 1) - 1) & 1)) {
+          *a.status = kDevTimeoutMma;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dcol = tmem + buf * kGgCols;
+        for (int kb = 0; kb < n; ++kb, ++i) {
+          const int s = i % S, j = i % R;
+          // both CTAs' expanding warps arrived: both copies landed and both operands are written
+          if (!mbar_wait_cluster(&opready[j], (i / R) & 1)) {
+            *a.status = kDevTimeoutMma;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ua = smem_u32(sA + s * C::A_STAGE), ub = smem_u32(sOp + j * C::OP);
 #pragma unroll
-    for (int d = 0; d < 16; ++d)
+          for (int kk = 0; kk < kGgRed / 16; ++kk) {
+            const uint64_t ad = kWeight ? smem_desc_sw128_mnmajor(ua + kk * 2048, 8192)
+                                        : smem_desc_sw128_kmajor(ua) + static_cast<uint64_t>(kk * 2);
+            tc_mma_f16_ss_pair(dcol, ad, smem_desc_sw128_mnmajor(ub + kk * 2048, 8192), C::IDESC,
+                               (kb | kk) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair_mc(&empty[s], 0x3);  // frees copy stage s, and operand slot j for k-block i + R
+          issued = true;
+        }
+        if (ok) tc_commit_pair_mc(&accfull[buf], 0x3);
+      }
+      if (!ok && issued) {
+        tc_commit_pair(drain);
+        if (!mbar_wait(drain, 0)) *a.status = kDevTimeoutDrain;
+      }
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // -------------------------------------------------------------- expansion (both CTAs)
+    // Eight lanes take a line's 128 columns, 16 each; lanes 4 .. 7 (the second
+    // block of 64) store their odd chunk first, so the eight 16-byte stores of a
+    // line fall into eight bank groups.
+    const int grp = (warp - 4) >> 2;
+    const int tid = (warp & 3) * 32 + lane;
+    const int jc = tid & 7, line0 = tid >> 3;  // lines line0 + 16 u
+    const int c0 = 2 * (jc & 3) + (jc >> 2), c1 = 2 * (jc & 3) + 1 - (jc >> 2);
+    int i = 0;
+    bool ok = true;
+    for (int g = pair; g < a.units && ok; g += npairs) {
+      int row0, col0, kb0;
+      const int n = unit_of(g, row0, col0, kb0);
+      for (int kb = kb0; kb < kb0 + n; ++kb, ++i) {
+        if ((i & 1) != grp) continue;
+        const int s = i % S, j = i % R;
+        float sc[4];
+        if (kWeight) {  // the tokens' scales, read while the copy is in flight
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+          for (int u = 0; u < 4; ++u) {
+            const int m = kb * kGgRed + line0 + 16 * u;
+            sc[u] = m < a.red ? a.gamma[m] : 0.0f;
+          }
+        }
+        if (!mbar_wait(&full[s], (i / S) & 1) || (i >= R && !mbar_wait(&empty[(i - R) % S], ((i - R) / S) & 1))) {
+          *a.status = kDevTimeoutUnpack;
+          ok = false;
+          break;
+        }
+        const uint8_t* raw = sRaw + s * C::RAW;
+        uint8_t* op = sOp + j * C::OP + (jc >> 2) * 8192;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sA[d][ty * 4 + i], sB[d][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+        for (int u = 0; u < 4; ++u) {
+          const int line = line0 + 16 * u;
+          uint32_t o[8];
+          if (kWeight) {
+            const uint4 q = *reinterpret_cast<const uint4*>(raw + line * 128 + jc * 16);
+            const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+            const float sv = __fdiv_rn(sc[u], kQb);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float f[4];
+              codes4_f32(qw[e], f);
+              o[2 * e] = pack_bf16x2(__fmul_rn(f[0], sv), __fmul_rn(f[1], sv));
+              o[2 * e + 1] = pack_bf16x2(__fmul_rn(f[2], sv), __fmul_rn(f[3], sv));
+            }
+          } else {
+            ternary16_bf16(*reinterpret_cast<const uint32_t*>(raw + line * 32 + jc * 4), o);
+          }
+          uint8_t* dst = op + line * 128;
+          const bool odd = jc >= 4;
+          *reinterpret_cast<uint4*>(dst + ((c0 ^ (line & 7)) << 4)) =
+              odd ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dst + ((c1 ^ (line & 7)) << 4)) =
+              odd ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_cta(opready0 + static_cast<uint32_t>(j * 8));
+      }
+    }
+  } else if (warp >= 12) {
+    // -------------------------------------------------------------- stores (both CTAs, own rows)
+    const int q = warp - 12;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const float alpha = kWeight ? 1.0f : *a.alpha;
+    int t = 0;
+    for (int g = pair; g < a.units; g += npairs, ++t) {
+      const int buf = t & 1;
+      int row0, col0, kb0;
+      unit_of(g, row0, col0, kb0);
+      const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
+      if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
+        *a.status = kDevTimeoutEpilogue;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < kGgCols; c0 += 32) {
+        uint32_t w[32];
+        tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
+        tc_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c)  // dx: accumulator column 2 i + h of a 16-group is output column i + 8 h
+          v[kWeight ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
+        if (g >= a.full && a.split > 1) {
+          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + lrow * kGgCols + c0;
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) st_global_v8(p + c, reinterpret_cast<const uint32_t*>(v + c));
+        } else if (row0 + lrow < a.rows && col0 + c0 < a.cols) {
+          grad_store32<kWeight>(a, row0 + lrow, col0 + c0, v, alpha);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_cta(accempty0 + static_cast<uint32_t>(buf * 8));
+    }
   }
-  const float alpha = kWeight ? 1.0f : *a.alpha;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + ty * 4 + i, c = c0 + tx + 16 * j;
-      if (r >= rows || c >= cols) continue;
-      const int64_t at = static_cast<int64_t>(r) * cols + c;
-      if (kWeight) {
-        a.dw[at] = acc[i][j] + (a.accumulate ? a.dw[at] : 0.0f);
-      } else {
-        float v = __fmul_rn(acc[i][j], alpha);
-        if (a.add) v = __fadd_rn(v, bf16_bits_to_f32(a.add[at]));
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        a.dx[at] = *reinterpret_cast<const uint16_t*>(&h);
-      }
+  tc_fence_before();
+  __syncthreads();
+  pdl_launch_dependents();
+  cluster_sync_all();  // no remote arrive or multicast commit is left in flight towards either CTA
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// The split tiles: adds each tile's parts in order and finishes it.  A thread
+// takes 32 columns of a row, as the storing warps do.
+template <bool kWeight>
+__global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int unit = blockIdx.x >> 3;                                  // split tile
+  const int e = (blockIdx.x & 7) * 256 + threadIdx.x;                // 2048 (row, 32 columns) of a tile
+  const int tile = a.full + unit;
+  const int rt = tile / a.col_tiles;
+  const int lrow = e >> 3, lc = (e & 7) * 32;
+  const int64_t row = static_cast<int64_t>(rt) * kGgRows + lrow;
+  const int col = (tile - rt * a.col_tiles) * kGgCols + lc;
+  if (row >= a.rows || col >= a.cols) return;
+  const float* p = a.slab + static_cast<size_t>(unit) * a.split * kGgSlab + lrow * kGgCols + lc;
+  float v[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+  for (int s = 0; s < a.split; ++s, p += kGgSlab) {
+    uint32_t w[32];
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) ld_global_v8(p + c, w + c);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = __fadd_rn(v[c], __uint_as_float(w[c]));
+  }
+  grad_store32<kWeight>(a, row, col, v, kWeight ? 1.0f : *a.alpha);
+}
+
+// ----------------------------------------------------------------- operands put in order
+// Rows whose stride TMA cannot step (not a multiple of 16 bytes), copied to rows that it can; T: 2-byte or 1-byte.
+template <typename T>
+__global__ void __launch_bounds__(256) pad_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t rows, int cols,
+                                                       T* __restrict__ dst, int64_t ldd) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256) dst[r * ldd + c] = src[r * ld + c];
+}
+
+// N:M rows expanded to dense codes (16 weights a thread), the layout of the
+// dense matrix of the same size; positions past K hold code 1.
+struct NmExpandArgs {
+  const uint8_t* codes;
+  const uint8_t* meta;
+  int64_t ldc, ldm, ldd;
+  int N, K, nm_n, nm_m;
+  uint32_t* out;
+};
+__global__ void __launch_bounds__(256) nm_expand_kernel(const NmExpandArgs a) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int words = static_cast<int>(a.ldd / 4);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= static_cast<int64_t>(a.N) * words) return;
+  const int64_t n = at / words;
+  const int k0 = static_cast<int>(at - n * words) * 16;
+  const uint8_t* c = a.codes + n * a.ldc;
+  const uint8_t* mt = a.meta + n * a.ldm;
+  uint32_t o = 0x55555555u;
+  auto kept = [&](int pos) { return static_cast<uint32_t>(c[pos >> 2] >> (2 * (pos & 3))) & 3u; };
+  if (a.nm_m == 4) {
+    for (int b = k0 / 4; b < k0 / 4 + 4 && 4 * b < a.K; ++b) {
+      const uint32_t nib = mt[b >> 1] >> (4 * (b & 1));
+      const int s0 = 2 * (4 * b - k0 + static_cast<int>(nib & 3u)), s1 = 2 * (4 * b - k0 + static_cast<int>((nib >> 2) & 3u));
+      o = (o & ~(3u << s0)) | (kept(2 * b) << s0);
+      o = (o & ~(3u << s1)) | (kept(2 * b + 1) << s1);
     }
+  } else {
+    for (int b = k0 / 8; b < k0 / 8 + 2 && 8 * b < a.K; ++b) {
+      const uint32_t mask = mt[b];
+      int pos = b * a.nm_n;
+      for (int j = 0; j < 8; ++j)
+        if ((mask >> j) & 1u) {
+          const int sh = 2 * (8 * b - k0 + j);
+          if (pos < (b + 1) * a.nm_n) o = (o & ~(3u << sh)) | (kept(pos) << sh);
+          ++pos;
+        }
+    }
+  }
+  a.out[at] = o;
 }
 
 }  // namespace bl
