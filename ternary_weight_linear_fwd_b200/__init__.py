@@ -414,26 +414,49 @@ def forward_norm(w: PackedWeights, x, g, eps: float, want_acc: bool = False, fla
 # a call are on one device, which need not be the current one; work goes to `stream` or that device's current
 # stream, and what the call allocates belongs to the stream it runs on.
 
+class _Here:
+    """The empty context, for calls on the current device and stream."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_CTX = _Here()
+
+
 def _on(device, stream):
     """Context in which a call's outputs and workspace are allocated and its kernels are launched."""
     import torch
     if stream is None:
+        if device.type == "cuda" and device.index == torch.cuda.current_device():
+            return _HERE_CTX  # entering torch.cuda.device costs more than a small kernel
         return torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream on {stream.device} for tensors on {device}")
     return torch.cuda.stream(stream)
 
 
+def _raw_stream(device, stream) -> int:
+    """The address of `stream`, or of the device's current stream (without building a Stream object for it)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _mat(t, what: str, dtype, device=None, shape=None, align: int = 1):
     """A 2-D CUDA matrix as the kernels read it: (the tensor, its row stride).  Views with unit stride inside a
     row and rows that do not overlap pass as they are; others (expanded, transposed, misaligned) are copied."""
     import torch
-    if not (torch.is_tensor(t) and t.is_cuda and t.dtype == dtype and t.dim() == 2):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == 2):
         raise ValueError(f"{what}: expected a 2-D {dtype} CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{what}: expected a tensor on {device}, got one on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous() and t.data_ptr() % align == 0:
+        return t, t.shape[1]
     M, K = t.shape
     ok = (K == 1 or t.stride(1) == 1) and (M == 1 or t.stride(0) >= K) and t.data_ptr() % align == 0
     if not ok:
@@ -441,10 +464,17 @@ def _mat(t, what: str, dtype, device=None, shape=None, align: int = 1):
     return t, (t.stride(0) if M > 1 else K)
 
 
+def _new(like, dtype=None):
+    """An uninitialised contiguous tensor of the same shape and device."""
+    import torch
+    return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _vec(t, what: str, n: int, device, dtype=None):
     import torch
     dtype = dtype or torch.float32
-    if not (torch.is_tensor(t) and t.dtype == dtype and t.device == device and tuple(t.shape) == (n,)):
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == 1 and t.shape[0] == n
+            and t.device == device):
         raise ValueError(f"{what}: expected a {dtype} tensor of {n} elements on {device}")
     return t.contiguous()
 
@@ -468,11 +498,11 @@ def layernorm(x, weight, bias=None, eps: float = 1e-5, want_stats: bool = False,
         weight = _vec(weight, "weight", K, x.device)
         bias = None if bias is None else _vec(bias, "bias", K, x.device)
         _check_out(out, (M, K), torch.bfloat16, x.device, "out")
-        y = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        y = out if out is not None else _new(x)
         mean = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        rstd = _new(mean) if want_stats else None
         _check(lib().bitlinear_layernorm(_ptr(x), ldx, M, K, _ptr(weight), _ptr(bias), float(eps), _ptr(y),
-                                         _ptr(mean), _ptr(rstd), _stream(stream)), "layernorm")
+                                         _ptr(mean), _ptr(rstd), _raw_stream(x.device, stream)), "layernorm")
     return (y, mean, rstd) if want_stats else y
 
 
@@ -486,13 +516,13 @@ def layernorm_quant_act(x, weight, bias=None, eps: float = 1e-5, rowsum: bool = 
         M, K = x.shape
         weight = _vec(weight, "weight", K, x.device)
         bias = None if bias is None else _vec(bias, "bias", K, x.device)
-        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        q = _new(x, torch.int8)
         g = torch.empty(M, dtype=torch.float32, device=x.device)
-        rs = torch.empty(M, dtype=torch.int32, device=x.device) if rowsum else None
-        mean = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        rs = _new(g, torch.int32) if rowsum else None
+        mean = _new(g) if want_stats else None
+        rstd = _new(g) if want_stats else None
         _check(lib().bitlinear_layernorm_quant_act(_ptr(x), ldx, M, K, _ptr(weight), _ptr(bias), float(eps), _ptr(q),
-                                                   _ptr(g), _ptr(rs), _ptr(mean), _ptr(rstd), _stream(stream)),
+                                                   _ptr(g), _ptr(rs), _ptr(mean), _ptr(rstd), _raw_stream(x.device, stream)),
                "layernorm_quant_act")
     return (q, g, rs, mean, rstd) if want_stats else (q, g, rs)
 
@@ -511,13 +541,12 @@ def layernorm_backward(dy, x, weight, mean, rstd, want_bias: bool = True, worksp
         dy, lddy = _mat(dy, "dy", torch.bfloat16, x.device, (M, K))
         weight = _vec(weight, "weight", K, x.device)
         mean, rstd = _vec(mean, "mean", M, x.device), _vec(rstd, "rstd", M, x.device)
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-        dw = torch.empty(K, dtype=torch.float32, device=x.device)
-        db = torch.empty(K, dtype=torch.float32, device=x.device) if want_bias else None
+        dx, dw = _new(x), _new(weight)
+        db = _new(weight) if want_bias else None
         workspace, n = _scratch(workspace, norm_backward_workspace_bytes(M, K), x.device)
         _check(lib().bitlinear_layernorm_backward(_ptr(dy), lddy, _ptr(x), ldx, M, K, _ptr(weight), _ptr(mean),
                                                   _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), n,
-                                                  _stream(stream)), "layernorm_backward")
+                                                  _raw_stream(x.device, stream)), "layernorm_backward")
     return dx, dw, db
 
 
@@ -529,11 +558,10 @@ def rmsnorm_backward(dy, x, g, eps: float, workspace=None, stream=None):
         M, K = x.shape
         dy, lddy = _mat(dy, "dy", torch.bfloat16, x.device, (M, K))
         g = _vec(g, "g", K, x.device)
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-        dg = torch.empty(K, dtype=torch.float32, device=x.device)
+        dx, dg = _new(x), _new(g)
         workspace, n = _scratch(workspace, norm_backward_workspace_bytes(M, K), x.device)
         _check(lib().bitlinear_rmsnorm_backward(_ptr(dy), lddy, _ptr(x), ldx, M, K, _ptr(g), float(eps), _ptr(dx),
-                                                _ptr(dg), _ptr(workspace), n, _stream(stream)), "rmsnorm_backward")
+                                                _ptr(dg), _ptr(workspace), n, _raw_stream(x.device, stream)), "rmsnorm_backward")
     return dx, dg
 
 
@@ -545,8 +573,8 @@ def dequant_act(q, gamma, out=None, stream=None):
         M, K = q.shape
         gamma = _vec(gamma, "gamma", M, q.device)
         _check_out(out, (M, K), torch.bfloat16, q.device, "out")
-        y = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
-        _check(lib().bitlinear_dequant_act(_ptr(q), ldq, _ptr(gamma), M, K, _ptr(y), _stream(stream)), "dequant_act")
+        y = out if out is not None else _new(q, torch.bfloat16)
+        _check(lib().bitlinear_dequant_act(_ptr(q), ldq, _ptr(gamma), M, K, _ptr(y), _raw_stream(q.device, stream)), "dequant_act")
     return y
 
 
@@ -570,12 +598,12 @@ def relu2_glu_quant_act(g, u, stream=None) -> Relu2GluCheckpoint:
         g, ldg = _mat(g, "g", torch.bfloat16)
         M, N = g.shape
         u, ldu = _mat(u, "u", torch.bfloat16, g.device, (M, N))
-        q = [torch.empty((M, N), dtype=torch.int8, device=g.device) for _ in range(3)]
-        m = [torch.empty(M, dtype=torch.float32, device=g.device) for _ in range(3)]
-        rs = torch.empty(M, dtype=torch.int32, device=g.device)
+        q0 = _new(g, torch.int8)
+        m0 = torch.empty(M, dtype=torch.float32, device=g.device)
+        q, m, rs = (q0, _new(q0), _new(q0)), (m0, _new(m0), _new(m0)), _new(m0, torch.int32)
         _check(lib().bitlinear_relu2_glu_quant_act(_ptr(g), ldg, _ptr(u), ldu, M, N, _ptr(q[0]), _ptr(m[0]),
                                                    _ptr(q[1]), _ptr(m[1]), _ptr(q[2]), _ptr(m[2]), _ptr(rs),
-                                                   _stream(stream)), "relu2_glu_quant_act")
+                                                   _raw_stream(g.device, stream)), "relu2_glu_quant_act")
     return Relu2GluCheckpoint(q[0], m[0], q[1], m[1], q[2], m[2], rs)
 
 
@@ -588,9 +616,9 @@ def relu2_glu_backward(dh, q_g, gamma_g, q_u, gamma_u, stream=None):
         _check_out(q_g, (M, N), torch.int8, dh.device, "q_g")
         _check_out(q_u, (M, N), torch.int8, dh.device, "q_u")
         gamma_g, gamma_u = _vec(gamma_g, "gamma_g", M, dh.device), _vec(gamma_u, "gamma_u", M, dh.device)
-        dg, du = (torch.empty((M, N), dtype=torch.bfloat16, device=dh.device) for _ in range(2))
+        dg, du = _new(dh), _new(dh)
         _check(lib().bitlinear_relu2_glu_backward(_ptr(dh), lddh, _ptr(q_g), _ptr(gamma_g), _ptr(q_u), _ptr(gamma_u),
-                                                  M, N, _ptr(dg), _ptr(du), _stream(stream)), "relu2_glu_backward")
+                                                  M, N, _ptr(dg), _ptr(du), _raw_stream(dh.device, stream)), "relu2_glu_backward")
     return dg, du
 
 
@@ -620,7 +648,7 @@ def backward_weight(dy, q, gamma, out=None, accumulate: bool = False, workspace=
         workspace, n = _scratch(workspace, backward_weight_workspace_bytes(M, N, K, lddy, ldq), dy.device)
         _check(lib().bitlinear_backward_weight(_ptr(dy), lddy, _ptr(q), ldq, _ptr(gamma), M, N, K, _ptr(dW),
                                                _ptr(workspace), n, FLAG_ACCUMULATE if accumulate else 0,
-                                               _stream(stream)), "backward_weight")
+                                               _raw_stream(dy.device, stream)), "backward_weight")
     return dW
 
 
@@ -646,7 +674,7 @@ def backward_input(w: PackedWeights, dy, add=None, out=None, workspace=None, str
         workspace, n = _scratch(workspace, backward_input_workspace_bytes(w, M, lddy), dy.device)
         ws = w.c_struct()
         _check(lib().bitlinear_backward_input(ctypes.byref(ws), _ptr(dy), lddy, M, _ptr(add), _ptr(dx),
-                                              _ptr(workspace), n, _stream(stream)), "backward_input")
+                                              _ptr(workspace), n, _raw_stream(dy.device, stream)), "backward_input")
     return dx
 
 

@@ -310,6 +310,12 @@ __device__ __forceinline__ void ld_global_v8(const void* p, uint32_t* r) {
                : "memory");
 }
 
+__device__ __forceinline__ void ld_global_nc_v8(const void* p, uint32_t* r) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "l"(p));
+}
+
 // d = c + sum_i a.u8[i] * b.s8[i]
 __device__ __forceinline__ int32_t dp4a_us(uint32_t a, uint32_t b, int32_t c) {
   int32_t d;

@@ -7,6 +7,10 @@
 namespace bl {
 namespace {
 
+// Most 8-wide chunks of a row that a lane of the row kernels keeps in registers.
+constexpr int kLnMaxChunks = 10;
+constexpr int kGluMaxChunks = 6;
+
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
@@ -14,30 +18,53 @@ bitlinear_status check_rows(int M, int K) {
   return M < 1 || M > BITLINEAR_MAX_M || K < 1 || K > BITLINEAR_MAX_K ? BITLINEAR_ERR_SHAPE : BITLINEAR_OK;
 }
 
-// Threads a row for the element-wise kernels of 16 values a thread and step.
-int row_lanes(int K) {
+// Threads a row for the element-wise kernels of 16 values a thread and step: at most `steps` steps, since each
+// step's loads are independent of the last one's and rows seldom divide into many threads evenly (4096 x 2560:
+// the restored activation 8.8 us with eight steps, 9.6 with four; the gate's gradients 17.8 and 16.8).
+int row_lanes(int M, int K, int steps, int sm_count) {
   int lanes = 32;
-  while (lanes < 256 && 16 * lanes < K) lanes *= 2;
+  while (lanes < 256 && 16 * lanes < K &&
+         (steps * 16 * lanes < K || static_cast<int64_t>(M) * lanes * steps < 4096ll * sm_count))
+    lanes *= 2;
   return lanes;
 }
 
-// Warps a row as quant_shape picks them, at most G 16-wide groups a lane kept in registers where it fits.
+// Warps a row: the fewest that keep it in registers (at most G 8-wide chunks a lane), more while the rows are few.
 int row_warps(int M, int K, int G, int sm_count) {
-  const int groups = (K + 15) / 16;
+  const int chunks = (K + 7) / 8;
   int wpr = 1;
-  while (wpr < kQuantWarps && (groups > G * 32 * wpr || static_cast<int64_t>(M) * wpr < 24ll * sm_count)) wpr *= 2;
+  while (wpr < kQuantWarps && (chunks > G * 32 * wpr ||
+                               (static_cast<int64_t>(M) * wpr < 12ll * sm_count && chunks > 32 * wpr)))
+    wpr *= 2;
   return wpr;
 }
+int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v / 2); }
+int row_chunks(int K, int wpr) { return ((K + 7) / 8 + 32 * wpr - 1) / (32 * wpr); }
+
+// Rows of K bf16, ld apart, that 16-byte accesses can take.
+bool rows16(const void* p, int64_t ld, int K) { return K % 8 == 0 && ld % 8 == 0 && aligned16(p); }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 template <bool kCodes>
 bitlinear_status layernorm_launch(LnArgs a, cudaStream_t s, int sm_count) {
-  a.wpr = row_warps(a.M, a.K, 3, sm_count);
-  const int need = ((a.K + 15) / 16 + 32 * a.wpr - 1) / (32 * a.wpr);
-  const int rpc = kQuantWarps / a.wpr;
+  const int wpr = row_warps(a.M, a.K, kLnMaxChunks, sm_count);
+  a.lw = log2i(wpr);
+  a.inv_k = 1.0 / a.K;
+  const bool fast = rows16(a.x, a.ldx, a.K) && aligned32(a.w) && aligned32(a.b) && aligned16(a.y) && aligned8(a.q);
+  const int need = fast ? row_chunks(a.K, wpr) : kLnMaxChunks + 1;
+  const int rpc = kQuantWarps / wpr;
   const dim3 grid((a.M + rpc - 1) / rpc), block(32 * kQuantWarps);
-  if (need <= 1) return launch(layernorm_kernel<kCodes, 1>, grid, block, 0, s, false, a);
-  if (need <= 2) return launch(layernorm_kernel<kCodes, 2>, grid, block, 0, s, false, a);
-  return launch(layernorm_kernel<kCodes, 3>, grid, block, 0, s, false, a);
+  auto go = [&](auto kern) { return launch(kern, grid, block, 0, s, false, a); };
+  if (need <= 1) return go(layernorm_kernel<kCodes, 1>);
+  if (need <= 2) return go(layernorm_kernel<kCodes, 2>);
+  if (need <= 3) return go(layernorm_kernel<kCodes, 3>);
+  if (need <= 4) return go(layernorm_kernel<kCodes, 4>);
+  if (need <= 5) return go(layernorm_kernel<kCodes, 5>);
+  if (need <= 6) return go(layernorm_kernel<kCodes, 6>);
+  if (need <= 8) return go(layernorm_kernel<kCodes, 8>);
+  if (need <= kLnMaxChunks) return go(layernorm_kernel<kCodes, kLnMaxChunks>);
+  return go(layernorm_kernel<kCodes, 0>);
 }
 
 bitlinear_status check_layernorm(const LnArgs& a) {
@@ -56,6 +83,8 @@ struct NbPlan {
   int G, T, rg, ctas;
 };
 
+// Two chunks a thread, four where rows are too long for that; one where the rows are few (a short chain counts) or
+// would leave more than a sixth of two-chunk threads idle.
 NbPlan nb_plan(int M, int K, int sm_count) {
   NbPlan p;
   const int chunks = (K + 7) / 8;
@@ -64,9 +93,11 @@ NbPlan nb_plan(int M, int K, int sm_count) {
     p.ctas = std::min(M, 64);
     return p;
   }
-  p.G = chunks <= kNbMaxThreads ? 1 : 2;
-  p.T = ((chunks + p.G - 1) / p.G + 31) / 32 * 32;
-  p.rg = std::max(1, std::min({kNbMaxGroups, kNbMaxThreads / p.T, (M + sm_count - 1) / sm_count}));
+  auto threads = [&](int G) { return ((chunks + G - 1) / G + 31) / 32 * 32; };
+  p.G = threads(2) <= nb_max_threads(2) ? 2 : 4;
+  if (threads(1) <= nb_max_threads(1) && (M <= 4 * sm_count || 5 * 2 * threads(2) > 6 * threads(1))) p.G = 1;
+  p.T = threads(p.G);  // (G - 1) T < chunks: with G = 2 since more than 32 chunks, with G = 4 since more than 1024
+  p.rg = std::max(1, std::min({kNbMaxGroups, nb_max_threads(p.G) / p.T, (M + sm_count - 1) / sm_count}));
   p.ctas = std::min(sm_count, (M + p.rg - 1) / p.rg);
   return p;
 }
@@ -85,9 +116,12 @@ bitlinear_status norm_backward(NbArgs a, float* dw, float* db, void* ws, size_t 
   a.rg = p.rg;
   bitlinear_status st;
   if (p.T) {
-    const size_t smem = 4 * (static_cast<size_t>(8) * p.G * p.T + (p.rg > 1 ? a.K : 0));
-    st = p.G == 1 ? launch(norm_backward_kernel<kLayer, 1>, dim3(p.ctas), dim3(p.T * p.rg), smem, s, false, a)
-                  : launch(norm_backward_kernel<kLayer, 2>, dim3(p.ctas), dim3(p.T * p.rg), smem, s, false, a);
+    const size_t smem = static_cast<size_t>(32) * p.G * nb_max_threads(p.G) * (p.rg > 1 ? 2 : 1);
+    auto go = [&](auto kern) { return launch(kern, dim3(p.ctas), dim3(p.T * p.rg), smem, s, false, a); };
+    const bool fast = rows16(a.x, a.ldx, a.K) && rows16(a.dy, a.lddy, a.K) && aligned16(a.dx);
+    st = p.G == 1   ? go(fast ? norm_backward_kernel<kLayer, true, 1> : norm_backward_kernel<kLayer, false, 1>)
+         : p.G == 2 ? go(fast ? norm_backward_kernel<kLayer, true, 2> : norm_backward_kernel<kLayer, false, 2>)
+                    : go(fast ? norm_backward_kernel<kLayer, true, 4> : norm_backward_kernel<kLayer, false, 4>);
   } else {
     float* r = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part);
     st = launch(norm_backward_long_kernel<kLayer>, dim3(a.M), dim3(1024), 0, s, false, a, r);
@@ -210,7 +244,6 @@ void gg_args(GradArgs* a, const GgPlan& p, int rows, int cols, int red, void* ws
 
 size_t bw_codes_bytes(int64_t M, int K, int64_t ldq) { return ldq % 16 ? static_cast<size_t>(M) * k16(K) : 0; }
 size_t bi_codes_bytes(int N, int K, int nm_m) { return nm_m ? static_cast<size_t>(N) * dense_ld(K) : 0; }
-inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 }  // namespace
 }  // namespace bl
@@ -343,7 +376,7 @@ bitlinear_status bitlinear_dequant_act(const int8_t* q, int64_t ldq, const float
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
-  const int lanes = row_lanes(K), rpc = 256 / lanes;
+  const int lanes = row_lanes(M, K, 8, dev->sm_count), rpc = 256 / lanes;
   st = launch(dequant_act_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, static_cast<cudaStream_t>(stream), false, q,
               ldq, gamma, M, K, y, lanes);
   if (st == BITLINEAR_OK) t_last_kernel = "dequant_act";
@@ -378,14 +411,22 @@ bitlinear_status bitlinear_relu2_glu_quant_act(const uint16_t* g, int64_t ldg, c
   a.gu = gamma_u;
   a.gh = gamma_h;
   a.rowsum = rowsum_h;
-  a.wpr = row_warps(M, N, 2, dev->sm_count);
-  const int need = ((N + 15) / 16 + 32 * a.wpr - 1) / (32 * a.wpr);
-  const int rpc = kQuantWarps / a.wpr;
-  const dim3 grid((M + rpc - 1) / rpc), block(32 * kQuantWarps);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = need <= 1   ? launch(relu2_glu_quant_kernel<1>, grid, block, 0, s, false, a)
-       : need <= 2 ? launch(relu2_glu_quant_kernel<2>, grid, block, 0, s, false, a)
-                   : launch(relu2_glu_quant_kernel<3>, grid, block, 0, s, false, a);
+  const int wpr = row_warps(M, N, kGluMaxChunks, dev->sm_count);
+  a.lw = log2i(wpr);
+  const bool fast = rows16(g, ldg, N) && rows16(u, ldu, N) && aligned8(q_g) && aligned8(q_u) && aligned8(q_h);
+  const int need = fast ? row_chunks(N, wpr) : kGluMaxChunks + 1;
+  const int rpc = kQuantWarps / wpr;
+  auto go = [&](auto kern) {
+    return launch(kern, dim3((M + rpc - 1) / rpc), dim3(32 * kQuantWarps), 0, static_cast<cudaStream_t>(stream), false,
+                  a);
+  };
+  st = need <= 1                ? go(relu2_glu_quant_kernel<1>)
+       : need <= 2              ? go(relu2_glu_quant_kernel<2>)
+       : need <= 3              ? go(relu2_glu_quant_kernel<3>)
+       : need <= 4              ? go(relu2_glu_quant_kernel<4>)
+       : need <= 5              ? go(relu2_glu_quant_kernel<5>)
+       : need <= kGluMaxChunks  ? go(relu2_glu_quant_kernel<kGluMaxChunks>)
+                                : go(relu2_glu_quant_kernel<0>);
   if (st == BITLINEAR_OK) t_last_kernel = "relu2_glu_quant_act";
   return st;
 }
@@ -402,7 +443,7 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
-  const int lanes = row_lanes(N), rpc = 256 / lanes;
+  const int lanes = row_lanes(M, N, 4, dev->sm_count), rpc = 256 / lanes;
   st = launch(relu2_glu_backward_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, static_cast<cudaStream_t>(stream),
               false, dh, lddh, q_g, gamma_g, q_u, gamma_u, M, N, dg, du, lanes);
   if (st == BITLINEAR_OK) t_last_kernel = "relu2_glu_backward";

@@ -344,10 +344,13 @@ __global__ void __launch_bounds__(kGgThreads, 1)
             const float sv = __fdiv_rn(sc[u], kQb);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float f[4];
+              float2 f[2];
               codes4_f32(qw[e], f);
-              o[2 * e] = pack_bf16x2(__fmul_rn(f[0], sv), __fmul_rn(f[1], sv));
-              o[2 * e + 1] = pack_bf16x2(__fmul_rn(f[2], sv), __fmul_rn(f[3], sv));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                f[h] = __fmul2_rn(f[h], splat2(sv));
+                o[2 * e + h] = pack_bf16x2(f[h].x, f[h].y);
+              }
             }
           } else {
             ternary16_bf16(*reinterpret_cast<const uint32_t*>(raw + line * 32 + jc * 4), o);

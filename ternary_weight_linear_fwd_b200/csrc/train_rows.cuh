@@ -11,17 +11,24 @@
 namespace bl {
 
 // ----------------------------------------------------------------- helpers
-// 16 fp32 parameters from k0 (zero past K).
-__device__ __forceinline__ void load16_f32(const float* p, int k0, int K, float (&v)[16]) {
-  if (k0 + 16 <= K && (reinterpret_cast<uintptr_t>(p + k0) & 15u) == 0) {
+// Everything here walks rows in chunks of 8 columns, 16 bytes of bf16 a lane,
+// and computes two columns an instruction (float2).
+
+__device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
+
+// 8 fp32 parameters from k0 (zero past K); one 32-byte load where p is 32-byte aligned.
+__device__ __forceinline__ void load8_f32(const float* p, int k0, int K, bool vec, float2 (&v)[4]) {
+  if (vec && k0 + 8 <= K) {
+    uint32_t r[8];
+    ld_global_nc_v8(p + k0, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 t = reinterpret_cast<const float4*>(p + k0)[i];
-      v[4 * i] = t.x; v[4 * i + 1] = t.y; v[4 * i + 2] = t.z; v[4 * i + 3] = t.w;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = k0 + i < K ? p[k0 + i] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = k0 + 2 * i < K ? p[k0 + 2 * i] : 0.0f;
+      v[i].y = k0 + 2 * i + 1 < K ? p[k0 + 2 * i + 1] : 0.0f;
+    }
   }
 }
 
@@ -32,6 +39,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float2 bf16_2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
 // 8 bf16 values at row[k0 ..], those past K left out.
 __device__ __forceinline__ void store8_bf16(uint16_t* row, int k0, int K, bool vec, const uint32_t* o) {
@@ -44,15 +52,14 @@ __device__ __forceinline__ void store8_bf16(uint16_t* row, int k0, int K, bool v
   }
 }
 
-// 16 codes at row[k0 ..], those past K left out.
-__device__ __forceinline__ void store16_codes(int8_t* row, int k0, int K, bool vec, const uint4 w) {
-  if (vec && k0 + 16 <= K) {
-    *reinterpret_cast<uint4*>(row + k0) = w;
+// 8 codes at row[k0 ..], those past K left out.
+__device__ __forceinline__ void store8_codes(int8_t* row, int k0, int K, bool vec, const uint2 w) {
+  if (vec && k0 + 8 <= K) {
+    *reinterpret_cast<uint2*>(row + k0) = w;
   } else {
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k0 + i < K) row[k0 + i] = static_cast<int8_t>(ww[i >> 2] >> (8 * (i & 3)));
+    for (int i = 0; i < 8; ++i)
+      if (k0 + i < K) row[k0 + i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
   }
 }
 
@@ -72,20 +79,50 @@ __device__ __forceinline__ void load16_codes(const int8_t* row, int k0, int K, b
   }
 }
 
-// 8 fp32 values of shared memory (16-byte aligned).
-__device__ __forceinline__ void load8_smem(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
 // Four int8 codes as fp32, exactly: the code plus 128 goes into the low byte
 // of 2^23, whose last place is 1.
-__device__ __forceinline__ void codes4_f32(uint32_t w, float (&f)[4]) {
+__device__ __forceinline__ void codes4_f32(uint32_t w, float2 (&f)[2]) {
   const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    f[j] = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + j)), 8388736.0f);
+  for (int j = 0; j < 2; ++j)
+    f[j] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + 2 * j)),
+                                  __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + 2 * j))),
+                      splat2(-8388736.0f));
+}
+
+// Four codes from the low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+  return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+}
+__device__ __forceinline__ int32_t code_sum(const uint2 w) {
+  return __dp4a(static_cast<int>(w.y), 0x01010101, __dp4a(static_cast<int>(w.x), 0x01010101, 0));
+}
+
+// The codes of 8 values by codes8f's division-free rounding, two values an
+// instruction.  emax grows to the largest distance to a code; past kCodesNear
+// some value lies so near the middle of two codes that codes8_exact has to
+// decide.  The two are apart because the exact one is long and rare (one chunk
+// in a thousand): inlined into every chunk's step it filled the instruction
+// cache (a fifth of the stalls of a 4096 x 2560 layer norm).
+constexpr float kCodesNear = 0.5f - 6.103515625e-05f;
+__device__ __forceinline__ uint2 codes8_near(const float2 (&v)[4], float c, float& emax) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 sm = __ffma2_rn(v[i], splat2(c), splat2(kMagic));
+    const float2 e = __ffma2_rn(v[i], splat2(-c), __fadd2_rn(sm, splat2(-kMagic)));
+    emax = fmaxf(emax, fmaxf(fabsf(e.x), fabsf(e.y)));
+    b[2 * i] = __float_as_uint(sm.x);
+    b[2 * i + 1] = __float_as_uint(sm.y);
+  }
+  return make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
+}
+__device__ __forceinline__ uint2 codes8_exact(const float2 (&v)[4], float d) {
+  uint32_t b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    b[e] = static_cast<uint32_t>(__float2int_rn(__fdiv_rn(__fmul_rn((e & 1) ? v[e >> 1].y : v[e >> 1].x, kQb), d)));
+  return make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
 }
 
 // ----------------------------------------------------------------- layer norm
@@ -93,7 +130,8 @@ __device__ __forceinline__ void codes4_f32(uint32_t w, float (&f)[4]) {
 // exact there, so the one-pass variance s2 - s1^2 / K loses nothing a two-pass
 // one would keep: 53 bits against the 24 of its result even at a mean of a
 // thousand deviations); mean = RN32(s1 / K), var = RN32(max(0, (s2 - s1^2 / K) /
-// K)), rstd = RN32(1 / sqrt(var + eps)) with root and quotient in fp64, and
+// K)), rstd = RN32(1 / sqrt(var + eps)), each computed in fp64 (1 / K rounded
+// there once, so that no quotient stands in a row's way), and
 //   xn = RN(RN(RN(x - mean) * rstd) * w) (+ RN b)
 // every operation one fp32 rounding, so that the codes are defined to the bit.
 struct LnArgs {
@@ -109,78 +147,79 @@ struct LnArgs {
   int32_t* rowsum;
   float* mean;     // or null
   float* rstd;     // or null
-  int wpr;         // warps per row
+  int lw;          // log2 of the warps per row
+  double inv_k;    // 1 / K
 };
 
-// A row belongs to wpr warps of a 256-thread CTA; a lane owns the 16-wide
-// groups g = sub * 32 + lane + j * 32 * wpr.  Rows of up to 16 G lanes * wpr
-// elements stay in registers between the three passes (moments, maximum,
-// output); longer or unaligned rows are read again, from L2.
+// A row belongs to wpr warps of a 256-thread CTA; a lane owns the 8-wide
+// chunks c = sub * 32 + lane + j * 32 * wpr, at most G of them, in registers:
+// the row is read once, all its loads in flight together, and with codes its
+// normalised values stay in registers between the maximum and the rounding, so
+// the parameters are read once a row as well (read twice, 16 columns a lane,
+// they filled the L1 pipe for 42 us at 4096 x 2560).  G > 0 needs rows and
+// parameters that 16- and 32-byte loads can take and K % 8 == 0: its steps are
+// loads are free of branches (chunks past K read the last one and are left out
+// of sums, maximum and output), so that those of several go out together.
+// G = 0: any row; it is read again for each pass, from L2.
 template <bool kCodes, int G>
-__global__ void __launch_bounds__(32 * kQuantWarps, G <= 3 ? 3 : 2) layernorm_kernel(const LnArgs a) {
+__global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) layernorm_kernel(const LnArgs a) {
+  constexpr bool kRegs = G > 0;
+  constexpr int GR = kRegs ? G : 1;
   __shared__ double s_s1[kQuantWarps], s_s2[kQuantWarps];
   __shared__ float s_mx[kQuantWarps];
   __shared__ int32_t s_sum[kQuantWarps];
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wpr = a.wpr, K = a.K;
-  const int rloc = warp / wpr, sub = warp - rloc * wpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantWarps / wpr) + rloc;
+  const int wpr = 1 << a.lw, K = a.K;
+  const int rloc = warp >> a.lw, sub = warp & (wpr - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantWarps >> a.lw) + rloc;
   const bool active = row < a.M;  // inactive warps still reach the CTA barriers
   const uint16_t* xr = a.x + (active ? row : 0) * a.ldx;
-  const bool vec_ok = (a.ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0;
-  const int groups = (K + 15) / 16;
-  const int gstride = 32 * wpr;
-  const int g0 = sub * 32 + lane;
-  const bool in_regs = groups <= G * gstride;
+  const bool xvec = kRegs || ((a.ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0);
+  const bool wvec = kRegs || (reinterpret_cast<uintptr_t>(a.w) & 31u) == 0;
+  const bool bvec = kRegs || (reinterpret_cast<uintptr_t>(a.b) & 31u) == 0;
+  const int chunks = (K + 7) / 8;
+  const int cstride = 32 * wpr;
+  const int c0 = sub * 32 + lane;
 
-  uint32_t v[G][8];
-  if (active && in_regs) {
+  uint32_t v[GR][4];
+  if (kRegs) {
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int g = g0 + j * gstride;
-      if (g < groups) {
-        uint32_t r0[4], r1[4];
-        load8_raw(xr, 16 * g, K, vec_ok, r0);
-        load8_raw(xr, 16 * g + 8, K, vec_ok, r1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[j][i] = r0[i];
-          v[j][4 + i] = r1[i];
-        }
-      }
+    for (int j = 0; j < GR; ++j) {
+      const int c = c0 + j * cstride;
+      const uint4 t = *reinterpret_cast<const uint4*>(xr + 8 * min(c, chunks - 1));
+      v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
     }
   }
-  auto for_groups = [&](auto&& f) {
-    if (!active) return;
-    if (in_regs) {
+  // f(j, chunk, its words) for each of the lane's chunks, and with G > 0 for those past K too
+  auto for_chunks = [&](auto&& f) {
+    if constexpr (kRegs) {
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-        if (g0 + j * gstride < groups) f(g0 + j * gstride, v[j]);
-    } else {
-      for (int g = g0; g < groups; g += gstride) {
-        uint32_t r0[4], r1[4];
-        load8_raw(xr, 16 * g, K, vec_ok, r0);
-        load8_raw(xr, 16 * g + 8, K, vec_ok, r1);
-        const uint32_t r[8] = {r0[0], r0[1], r0[2], r0[3], r1[0], r1[1], r1[2], r1[3]};
-        f(g, r);
+      for (int j = 0; j < GR; ++j) f(j, c0 + j * cstride, v[j]);
+    } else if (active) {
+      for (int c = c0; c < chunks; c += cstride) {
+        uint32_t r[4];
+        load8_raw(xr, 8 * c, K, xvec, r);
+        f(0, c, r);
       }
     }
   };
 
-  double s1 = 0.0, s2 = 0.0;
-  for_groups([&](int, const uint32_t (&r)[8]) {  // zero past K
+  double t1[2] = {0.0, 0.0}, t2[2] = {0.0, 0.0};  // two chains of additions each
+  for_chunks([&](int, int c, const uint32_t (&r)[4]) {  // zero past K
+    if (c >= chunks) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double lo = static_cast<double>(__uint_as_float(r[i] << 16));
-      const double hi = static_cast<double>(__uint_as_float(r[i] & 0xFFFF0000u));
-      s1 += lo;
-      s2 = __fma_rn(lo, lo, s2);
-      s1 += hi;
-      s2 = __fma_rn(hi, hi, s2);
+    for (int i = 0; i < 4; ++i) {
+      const double x[2] = {static_cast<double>(bf16_lo(r[i])), static_cast<double>(bf16_hi(r[i]))};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        t1[h] += x[h];
+        t2[h] = __fma_rn(x[h], x[h], t2[h]);
+      }
     }
   });
+  double s1 = t1[0] + t1[1], s2 = t2[0] + t2[1];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s1 += __shfl_xor_sync(0xffffffffu, s1, o);
@@ -198,51 +237,52 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G <= 3 ? 3 : 2) layernorm_ke
       s2 += s_s2[rloc * wpr + i];
     }
   }
-  const double kd = static_cast<double>(K);
-  const float mean = __double2float_rn(__ddiv_rn(s1, kd));
-  const double vard = __ddiv_rn(s2 - __ddiv_rn(s1 * s1, kd), kd);
+  const float mean = __double2float_rn(s1 * a.inv_k);
+  const double vard = (s2 - s1 * s1 * a.inv_k) * a.inv_k;
   const float var = __double2float_rn(vard < 0.0 ? 0.0 : vard);  // NaN stays NaN
-  const float rstd =
-      __double2float_rn(__ddiv_rn(1.0, __dsqrt_rn(static_cast<double>(var) + static_cast<double>(a.eps))));
+  const float rstd = __double2float_rn(rsqrt(static_cast<double>(var) + static_cast<double>(a.eps)));
   if (active && sub == 0 && lane == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
   }
 
-  // the group's normalised values; past K they are zero
-  auto normed = [&](int g, const uint32_t (&r)[8], float (&xn)[16]) {
-    float w[16], b[16];
-    load16_f32(a.w, 16 * g, K, w);
-    if (a.b) load16_f32(a.b, 16 * g, K, b);
+  // a chunk's normalised values
+  auto normed = [&](int c, const uint32_t (&r)[4], float2 (&xn)[4]) {
+    float2 w[4], b[4];
+    load8_f32(a.w, 8 * c, K, wvec, w);
+    if (a.b) load8_f32(a.b, 8 * c, K, bvec, b);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float x = __uint_as_float((e & 1) ? (r[e >> 1] & 0xFFFF0000u) : (r[e >> 1] << 16));
-      xn[e] = __fmul_rn(__fmul_rn(__fsub_rn(x, mean), rstd), w[e]);
-      if (a.b) xn[e] = __fadd_rn(xn[e], b[e]);
-    }
+    for (int i = 0; i < 4; ++i)
+      xn[i] = __fmul2_rn(__fmul2_rn(__fadd2_rn(bf16_2(r[i]), splat2(-mean)), splat2(rstd)), w[i]);
+    if (a.b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xn[i] = __fadd2_rn(xn[i], b[i]);
   };
+  const bool yvec = kRegs || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0);
+  const bool qvec = kRegs || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 7u) == 0);
 
   if (!kCodes) {
     uint16_t* yr = a.y + (active ? row : 0) * K;
-    const bool yvec = (K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0;
-    for_groups([&](int g, const uint32_t (&r)[8]) {
-      float xn[16];
-      normed(g, r, xn);
-      uint32_t o[8];
+    for_chunks([&](int, int c, const uint32_t (&r)[4]) {
+      float2 xn[4];
+      normed(kRegs ? min(c, chunks - 1) : c, r, xn);
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(xn[2 * i], xn[2 * i + 1]);
-      store8_bf16(yr, 16 * g, K, yvec, o);
-      store8_bf16(yr, 16 * g + 8, K, yvec, o + 4);
+      for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(xn[i].x, xn[i].y);
+      if (active && c < chunks) store8_bf16(yr, 8 * c, K, yvec, o);
     });
     return;
   }
 
+  float2 xs[kCodes ? GR : 1][4];  // kept between the passes (G > 0)
   float mx = 0.0f;
-  for_groups([&](int g, const uint32_t (&r)[8]) {
-    float xn[16];
-    normed(g, r, xn);
+  for_chunks([&](int j, int c, const uint32_t (&r)[4]) {
+    float2(&xn)[4] = xs[kCodes ? j : 0];
+    normed(kRegs ? min(c, chunks - 1) : c, r, xn);
+    float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(xn[e]));
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(xn[i].x), fabsf(xn[i].y)));
+    mx = c < chunks ? fmaxf(mx, m) : mx;
   });
   mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
   if (wpr > 1) {
@@ -251,18 +291,39 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G <= 3 ? 3 : 2) layernorm_ke
     for (int i = 0; i < wpr; ++i) mx = fmaxf(mx, s_mx[rloc * wpr + i]);
   }
   const float d = __fadd_rn(mx, kEps);
-  const float c = __fmul_rn(kQb, __frcp_rn(d));
+  const float c127 = __fmul_rn(kQb, __frcp_rn(d));
   int32_t sum = 0;
+  uint32_t redo = 0u;  // chunks whose codes take the exact quotient
   int8_t* qr = a.q + (active ? row : 0) * K;
-  const bool qvec = (K % 16) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0;
-  for_groups([&](int g, const uint32_t (&r)[8]) {
-    float xn[16];
-    normed(g, r, xn);
-    uint32_t b0[8], b1[8];
-    codes8f(xn, c, d, b0);
-    codes8f(xn + 8, c, d, b1);
-    store16_codes(qr, 16 * g, K, qvec, pack_group<false>(b0, b1, sum));
+  auto exact = [&](int c, const uint2 w0) {  // replaces w0, the chunk's codes
+    uint32_t r[4];
+    float2 xn[4];
+    load8_raw(xr, 8 * c, K, xvec, r);
+    normed(c, r, xn);
+    const uint2 w = codes8_exact(xn, d);
+    store8_codes(qr, 8 * c, K, qvec, w);
+    sum += code_sum(w) - code_sum(w0);
+  };
+  for_chunks([&](int j, int c, const uint32_t (&r)[4]) {
+    float2(&xn)[4] = xs[kCodes ? j : 0];
+    if (!kRegs) normed(c, r, xn);
+    float emax = 0.0f;
+    const uint2 w = codes8_near(xn, c127, emax);
+    if (!active || c >= chunks) return;
+    sum += code_sum(w);
+    store8_codes(qr, 8 * c, K, qvec, w);
+    if (emax > kCodesNear) {
+      if (kRegs)
+        redo |= 1u << j;
+      else
+        exact(c, w);
+    }
   });
+  while (kRegs && redo) {
+    const int c = c0 + (__ffs(redo) - 1) * cstride;
+    redo &= redo - 1;
+    exact(c, *reinterpret_cast<const uint2*>(qr + 8 * c));
+  }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (wpr > 1) {
     if (lane == 0) s_sum[warp] = sum;
@@ -287,6 +348,9 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G <= 3 ? 3 : 2) layernorm_ke
 // column sums of dw and db stay in its registers (fp32) until the end: x and
 // dy are read once.  Each CTA adds its groups' sums in order and writes one
 // partial row; norm_reduce_kernel adds the partial rows in a fixed order.
+// What a row costs beside its columns (two sums across the group, a barrier,
+// the quotients) is paid per warp, so few threads with several chunks each and
+// more groups beside each other beat one wide group.
 struct NbArgs {
   const uint16_t* dy;
   int64_t lddy;
@@ -302,39 +366,60 @@ struct NbArgs {
   int T, rg;
 };
 
-constexpr int kNbMaxThreads = 768;
-constexpr int kNbMaxGroups = 8;                       // one named barrier each
-constexpr int kNbMaxK = 2 * 8 * kNbMaxThreads;        // two chunks a thread; longer rows take the split kernels
+// Chunks a thread (G) and the most threads of a CTA, by what fits the registers:
+// 16 G of column sums (layer norm), 16 G of the row's values, 8 G of the next
+// row's words.  Measured (us, layer norm / RMSNorm, both launches):
+//   M x K          G = 1 (768)   G = 2 (512)   G = 4 (384)
+//   4096 x 2560    19.7 / 19.0   18.8 / 17.0   28.1 / 20.9
+//   256 x 2560      6.8 / 6.1     7.6 / 6.6    11.3 / 8.6
+//   8192 x 640     14.1 / 12.5   15.6 / 13.5   25.0 / 17.8
+//   999 x 11008        --        39.9 / 29.7 (768 threads)   39.3 / 24.6
+__host__ __device__ constexpr int nb_max_threads(int G) { return G == 1 ? 768 : G == 2 ? 512 : 384; }
+constexpr int kNbMaxGroups = 8;                                // one named barrier each
+constexpr int kNbMaxWarps = 24;                                // of a group
+constexpr int kNbMaxK = 8 * 4 * nb_max_threads(4);             // longer rows take the split kernels
 
-template <bool kLayer, int G>
-__global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const NbArgs a) {
-  extern __shared__ float s_nb[];  // [8 G T] the weight, zero past K; then [K] column sums handed from group to group
-  __shared__ float2 s_red[2][kNbMaxThreads / 32];
+// kFast: 16-byte accesses everywhere (columns past K, a whole chunk then, are read from the last chunk and zeroed).
+template <bool kLayer, bool kFast, int G>
+__global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(const NbArgs a) {
+  // [2][P] float4: the weight's columns 8 c .. 8 c + 3 and 8 c + 4 .. 8 c + 7 of each chunk, zero past K; then the
+  // same shape of column sums, handed from group to group (rg > 1)
+  extern __shared__ float4 s_nb[];
+  __shared__ __align__(16) float2 s_red[2][kNbMaxGroups][kNbMaxWarps];  // sums of a group's warps, then one zero
+  constexpr int P = G * nb_max_threads(G);  // float4 of a plane
+  constexpr bool kAhead = !(kLayer && G == 4);  // the next row's words fit the registers
   const int T = a.T, K = a.K;
-  float* s_w = s_nb;
-  float* s_acc = s_nb + 8 * G * T;
-  for (int k = threadIdx.x; k < 8 * G * T; k += blockDim.x) s_w[k] = k < K ? a.w[k] : 0.0f;
+  float4* s_acc = s_nb + 2 * P;
+  for (int k = threadIdx.x; k < 8 * G * T; k += blockDim.x)
+    reinterpret_cast<float*>(s_nb)[4 * ((k & 4 ? P : 0) + (k >> 3)) + (k & 3)] = k < K ? a.w[k] : 0.0f;
   const int grp = threadIdx.x / T, t = threadIdx.x - grp * T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int w0 = grp * (T / 32), nw = T / 32;
+  const int gw = warp - grp * (T / 32), nw = T / 32;
+  for (int i = threadIdx.x; i < 2 * kNbMaxGroups * kNbMaxWarps; i += blockDim.x) (&s_red[0][0][0])[i] = splat2(0.0f);
   const int chunks = (K + 7) / 8;
-  const bool vx = (a.ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0;
-  const bool vdy = (a.lddy % 8) == 0 && (reinterpret_cast<uintptr_t>(a.dy) & 15u) == 0;
-  const bool vdx = (K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 15u) == 0;
-  const float kf = static_cast<float>(K);
+  const bool vx = kFast || ((a.ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0);
+  const bool vdy = kFast || ((a.lddy % 8) == 0 && (reinterpret_cast<uintptr_t>(a.dy) & 15u) == 0);
+  const bool vdx = kFast || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 15u) == 0);
+  const float inv_k = __fdiv_rn(1.0f, static_cast<float>(K));
   const int64_t stride = static_cast<int64_t>(gridDim.x) * a.rg;
 
-  float dwv[G][8], dbv[G][8];
+  float2 dwv[G][4], dbv[G][4];
 #pragma unroll
   for (int j = 0; j < G; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwv[j][e] = dbv[j][e] = 0.0f;
-  uint32_t xw[G][4], yw[G][4], nx[G][4], ny[G][4];  // this row's words and the next one's
+    for (int i = 0; i < 4; ++i) dwv[j][i] = dbv[j][i] = splat2(0.0f);
+  uint32_t nx[G][4], ny[G][4];  // the next row's words
+  float nmean = 0.0f, nrstd = 1.0f;
   auto load = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int c = t + j * T;
-      if (c < chunks) {
+      if (kFast) {
+        const uint4 p = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + 8 * min(c, chunks - 1));
+        const uint4 q = *reinterpret_cast<const uint4*>(a.dy + row * a.lddy + 8 * min(c, chunks - 1));
+        nx[j][0] = p.x; nx[j][1] = p.y; nx[j][2] = p.z; nx[j][3] = p.w;
+        ny[j][0] = q.x; ny[j][1] = q.y; ny[j][2] = q.z; ny[j][3] = q.w;
+      } else if (c < chunks) {
         load8_raw(a.x + row * a.ldx, 8 * c, K, vx, nx[j]);
         load8_raw(a.dy + row * a.lddy, 8 * c, K, vdy, ny[j]);
       } else {
@@ -342,100 +427,123 @@ __global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const N
         for (int i = 0; i < 4; ++i) nx[j][i] = ny[j][i] = 0u;
       }
     }
+    if (kLayer) {
+      nmean = a.mean[row];
+      nrstd = a.rstd[row];
+    }
   };
-  auto el = [](const uint32_t (&w)[4], int e) { return (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]); };
+  auto weight = [&](int j, float2 (&w)[4]) {
+    const float4 p = s_nb[t + j * T], q = s_nb[P + t + j * T];
+    w[0] = make_float2(p.x, p.y);
+    w[1] = make_float2(p.z, p.w);
+    w[2] = make_float2(q.x, q.y);
+    w[3] = make_float2(q.z, q.w);
+  };
   __syncthreads();
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.rg + grp;
-  if (row < a.M) load(row);
+  if (kAhead && row < a.M) load(row);
   for (int it = 0; row < a.M; row += stride, it ^= 1) {
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xw[j][i] = nx[j][i];
-        yw[j][i] = ny[j][i];
-      }
-    if (row + stride < a.M) load(row + stride);  // in flight while this row's sums go round
-    float mean = 0.0f, rstd = 1.0f;
-    if (kLayer) {
-      mean = a.mean[row];
-      rstd = a.rstd[row];
-    }
-    float c1 = 0.0f, c2 = 0.0f;  // layer: sum a, sum a xh; RMS: sum x^2, sum a x
+    if (!kAhead) load(row);
+    const float mean = nmean;
+    float rstd = nrstd;
+    float2 xf[G][4], yf[G][4];  // layer: xh; RMS: x.  And dy
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      float w[8];
-      load8_smem(s_w + 8 * (t + j * T), w);
+      const bool past = kFast && j == G - 1 && t + j * T >= chunks;  // only the last chunk can be: (G - 1) T < chunks
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // past K the weight and dy are zero: nothing of such a column reaches a sum or is stored
-        const float x = el(xw[j], e), av = el(yw[j], e) * w[e];
-        c1 += kLayer ? av : x * x;
-        c2 = fmaf(av, kLayer ? (x - mean) * rstd : x, c2);
+      for (int i = 0; i < 4; ++i) {
+        xf[j][i] = bf16_2(past ? 0u : nx[j][i]);
+        yf[j][i] = bf16_2(past ? 0u : ny[j][i]);
+        if (kLayer) xf[j][i] = __fmul2_rn(__fadd2_rn(xf[j][i], splat2(-mean)), splat2(rstd));
       }
     }
+    if (kAhead && row + stride < a.M) load(row + stride);  // in flight while this row's sums go round
+    float2 p1 = splat2(0.0f), p2 = splat2(0.0f);  // layer: sum a, sum a xh; RMS: sum x^2, sum a x
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      float2 w[4];
+      weight(j, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // past K the weight and dy are zero: nothing of such a column reaches a sum or is stored
+        const float2 av = __fmul2_rn(yf[j][i], w[i]);
+        p1 = kLayer ? __fadd2_rn(p1, av) : __ffma2_rn(xf[j][i], xf[j][i], p1);
+        p2 = __ffma2_rn(av, xf[j][i], p2);
+      }
+    }
+    float c1 = p1.x + p1.y, c2 = p2.x + p2.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       c1 += __shfl_xor_sync(0xffffffffu, c1, o);
       c2 += __shfl_xor_sync(0xffffffffu, c2, o);
     }
-    if (lane == 0) s_red[it][warp] = make_float2(c1, c2);
-    bar_sync_n(1 + grp, T);  // one barrier a row: s_red[it] is written again only after the next row's barrier
-    c1 = c2 = 0.0f;
-    for (int i = 0; i < nw; ++i) {
-      const float2 v = s_red[it][w0 + i];
-      c1 += v.x;
-      c2 += v.y;
+    if (nw > 1) {
+      if (lane == 0) s_red[it][grp][gw] = make_float2(c1, c2);
+      bar_sync_n(1 + grp, T);  // one barrier a row: s_red[it] is written again only after the next row's barrier
+      c1 = c2 = 0.0f;
+      for (int i = 0; i < nw; i += 2) {
+        const float4 v = *reinterpret_cast<const float4*>(&s_red[it][grp][i]);
+        c1 += v.x + v.z;
+        c2 += v.y + v.w;
+      }
     }
-    c1 = __fdiv_rn(c1, kf);
-    c2 = __fdiv_rn(c2, kf);
+    c1 *= inv_k;
+    c2 *= inv_k;
     if (!kLayer) {
       rstd = __fdiv_rn(1.0f, __fsqrt_rn(c1 + a.eps));
-      c2 *= rstd;
+      c2 *= rstd * rstd;  // against x instead of xh
     }
+    uint16_t* dxr = a.dx + row * K;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int c = t + j * T;
-      float w[8];
-      load8_smem(s_w + 8 * c, w);
+      float2 w[4];
+      weight(j, w);
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int e = 2 * i + h;
-          const float xn = (el(xw[j], e) - mean) * rstd, dy = el(yw[j], e);  // RMS: mean = 0
-          float s = fmaf(dy, w[e], -xn * c2);
-          if (kLayer) s -= c1;
-          v[h] = s * rstd;
-          dwv[j][e] = fmaf(dy, xn, dwv[j][e]);
-          if (kLayer) dbv[j][e] += dy;
-        }
-        o[i] = pack_bf16x2(v[0], v[1]);
+        float2 s = __ffma2_rn(xf[j][i], splat2(-c2), __fmul2_rn(yf[j][i], w[i]));
+        if (kLayer) s = __fadd2_rn(s, splat2(-c1));
+        s = __fmul2_rn(s, splat2(rstd));
+        const float2 xh = kLayer ? xf[j][i] : __fmul2_rn(xf[j][i], splat2(rstd));
+        dwv[j][i] = __ffma2_rn(yf[j][i], xh, dwv[j][i]);
+        if (kLayer) dbv[j][i] = __fadd2_rn(dbv[j][i], yf[j][i]);
+        o[i] = pack_bf16x2(s.x, s.y);
       }
-      if (c < chunks) store8_bf16(a.dx + row * K, 8 * c, K, vdx, o);
+      if (c < chunks) store8_bf16(dxr, 8 * c, K, vdx, o);
     }
   }
   pdl_launch_dependents();
   // the groups' column sums, added in order of the groups; the last writes the CTA's partial row
 #pragma unroll
   for (int p = 0; p < (kLayer ? 2 : 1); ++p) {
+    float* out = a.part + (static_cast<size_t>(blockIdx.x) * (kLayer ? 2 : 1) + p) * K;
     for (int g = 0; g < a.rg; ++g) {
-      __syncthreads();
+      if (a.rg > 1) __syncthreads();
       if (g != grp) continue;
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = 8 * (t + j * T) + e;
-          if (k >= K) continue;
-          const float v = (p ? dbv[j][e] : dwv[j][e]) + (g > 0 ? s_acc[k] : 0.0f);
-          if (g + 1 < a.rg)
-            s_acc[k] = v;
-          else
-            a.part[(static_cast<size_t>(blockIdx.x) * (kLayer ? 2 : 1) + p) * K + k] = v;
+      for (int j = 0; j < G; ++j) {
+        const int c = t + j * T;
+        const float2(&s)[4] = p ? dbv[j] : dwv[j];
+        float4 lo = make_float4(s[0].x, s[0].y, s[1].x, s[1].y), hi = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+        if (g > 0) {
+          const float4 u = s_acc[c], v = s_acc[P + c];
+          lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
+          hi = make_float4(hi.x + v.x, hi.y + v.y, hi.z + v.z, hi.w + v.w);
         }
+        if (g + 1 < a.rg) {
+          s_acc[c] = lo;
+          s_acc[P + c] = hi;
+        } else if (K % 4 == 0 && 8 * c + 8 <= K) {
+          *reinterpret_cast<float4*>(out + 8 * c) = lo;
+          *reinterpret_cast<float4*>(out + 8 * c + 4) = hi;
+        } else {
+          const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (8 * c + e < K) out[8 * c + e] = v[e];
+        }
+      }
     }
   }
 }
@@ -552,10 +660,13 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const int8_t* __restri
     load16_codes(q + row * ldq, k0, K, qv, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float f[4];
+      float2 f[2];
       codes4_f32(w[i], f);
-      o[2 * i] = pack_bf16x2(__fmul_rn(f[0], s), __fmul_rn(f[1], s));
-      o[2 * i + 1] = pack_bf16x2(__fmul_rn(f[2], s), __fmul_rn(f[3], s));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f[h] = __fmul2_rn(f[h], splat2(s));
+        o[2 * i + h] = pack_bf16x2(f[h].x, f[h].y);
+      }
     }
     store8_bf16(y + row * K, k0, K, yv, o);
     store8_bf16(y + row * K, k0 + 8, K, yv, o + 4);
@@ -574,73 +685,80 @@ struct GluSaveArgs {
   int8_t *qg, *qu, *qh;                // [M, N]
   float *gg, *gu, *gh;                 // [M]
   int32_t* rowsum;                     // [M] sums of h's codes, or null
-  int wpr;
+  int lw;                              // log2 of the warps per row
 };
 
-// Warps and groups as in layernorm_kernel.
+// Warps and chunks as in layernorm_kernel; h is cheaper computed again (three
+// bf16x2 operations a pair) than kept.
 template <int G>
-__global__ void __launch_bounds__(32 * kQuantWarps, G <= 2 ? 3 : 2) relu2_glu_quant_kernel(const GluSaveArgs a) {
+__global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
+    relu2_glu_quant_kernel(const GluSaveArgs a) {
+  constexpr bool kRegs = G > 0;
+  constexpr int GR = kRegs ? G : 1;
   __shared__ uint32_t s_mx[3][kQuantWarps];
   __shared__ int32_t s_sum[kQuantWarps];
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wpr = a.wpr, N = a.N;
-  const int rloc = warp / wpr, sub = warp - rloc * wpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantWarps / wpr) + rloc;
+  const int wpr = 1 << a.lw, N = a.N;
+  const int rloc = warp >> a.lw, sub = warp & (wpr - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantWarps >> a.lw) + rloc;
   const bool active = row < a.M;
   const uint16_t* gr = a.g + (active ? row : 0) * a.ldg;
   const uint16_t* ur = a.u + (active ? row : 0) * a.ldu;
-  const bool vg = (a.ldg % 8) == 0 && (reinterpret_cast<uintptr_t>(a.g) & 15u) == 0;
-  const bool vu = (a.ldu % 8) == 0 && (reinterpret_cast<uintptr_t>(a.u) & 15u) == 0;
-  const int groups = (N + 15) / 16, gstride = 32 * wpr, g0 = sub * 32 + lane;
-  const bool in_regs = groups <= G * gstride;
+  const bool vg = kRegs || ((a.ldg % 8) == 0 && (reinterpret_cast<uintptr_t>(a.g) & 15u) == 0);
+  const bool vu = kRegs || ((a.ldu % 8) == 0 && (reinterpret_cast<uintptr_t>(a.u) & 15u) == 0);
+  const int chunks = (N + 7) / 8, cstride = 32 * wpr, c0 = sub * 32 + lane;
 
-  uint32_t v[G][16];  // g then u
-  auto load = [&](int g, uint32_t (&r)[16]) {
-    uint32_t t[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      load8_raw(h < 2 ? gr : ur, 16 * g + 8 * (h & 1), N, h < 2 ? vg : vu, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[4 * h + i] = t[i];
+  auto load = [&](int c, uint32_t (&r)[2][4]) {
+    if (kRegs) {
+      const uint4 t = *reinterpret_cast<const uint4*>(gr + 8 * c), y = *reinterpret_cast<const uint4*>(ur + 8 * c);
+      r[0][0] = t.x; r[0][1] = t.y; r[0][2] = t.z; r[0][3] = t.w;
+      r[1][0] = y.x; r[1][1] = y.y; r[1][2] = y.z; r[1][3] = y.w;
+    } else {
+      load8_raw(gr, 8 * c, N, vg, r[0]);
+      load8_raw(ur, 8 * c, N, vu, r[1]);
     }
   };
-  if (active && in_regs) {
+  uint32_t v[GR][2][4];  // g, u
+  if (kRegs) {
 #pragma unroll
-    for (int j = 0; j < G; ++j)
-      if (g0 + j * gstride < groups) load(g0 + j * gstride, v[j]);
+    for (int j = 0; j < GR; ++j) load(min(c0 + j * cstride, chunks - 1), v[j]);
   }
-  auto for_groups = [&](auto&& f) {
+  // f(j, chunk, its words) for each of the lane's chunks
+  auto for_chunks = [&](auto&& f) {
     if (!active) return;
-    if (in_regs) {
+    if constexpr (kRegs) {
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-        if (g0 + j * gstride < groups) f(g0 + j * gstride, v[j]);
+      for (int j = 0; j < GR; ++j)
+        if (c0 + j * cstride < chunks) f(j, c0 + j * cstride, v[j]);
     } else {
-      for (int g = g0; g < groups; g += gstride) {
-        uint32_t r[16];
-        load(g, r);
-        f(g, r);
+      for (int c = c0; c < chunks; c += cstride) {
+        uint32_t r[2][4];
+        load(c, r);
+        f(0, c, r);
       }
     }
   };
-  auto hword = [](uint32_t g, uint32_t u) {  // two elements
-    return relu2_glu_bf16(static_cast<uint16_t>(g), static_cast<uint16_t>(u)) |
-           (static_cast<uint32_t>(relu2_glu_bf16(static_cast<uint16_t>(g >> 16), static_cast<uint16_t>(u >> 16))) << 16);
+  auto as2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  auto bits = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); };
+  // two of h: each product is exact in more bits than bf16 keeps and is rounded once
+  auto hword = [&](uint32_t g, uint32_t u) {
+    const __nv_bfloat162 r = __hmax2(as2(g), as2(0u));  // NaN gives 0, as in the forward pass
+    return bits(__hmul2_rn(__hmul2_rn(r, r), as2(u)));
   };
-  // |x| as bit patterns order like the values
-  uint32_t mx[3] = {0u, 0u, 0u};
-  for_groups([&](int, const uint32_t (&r)[16]) {
+  uint32_t mx[3] = {0u, 0u, 0u};  // two maxima of |.| each; NaN is kept
+  for_chunks([&](int, int, const uint32_t (&r)[2][4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w[3] = {r[i], r[8 + i], hword(r[i], r[8 + i])};
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[3] = {r[0][i], r[1][i], hword(r[0][i], r[1][i])};
 #pragma unroll
-      for (int p = 0; p < 3; ++p) mx[p] = max(mx[p], max((w[p] << 16) & 0x7FFF0000u, w[p] & 0x7FFF0000u));
+      for (int p = 0; p < 3; ++p) mx[p] = bits(__hmax2_nan(as2(mx[p]), __habs2(as2(w[p]))));
     }
   });
 #pragma unroll
-  for (int p = 0; p < 3; ++p) mx[p] = __reduce_max_sync(0xffffffffu, mx[p]);
+  for (int p = 0; p < 3; ++p)  // |x| as bit patterns order like the values
+    mx[p] = __reduce_max_sync(0xffffffffu, max(mx[p] << 16, mx[p] & 0xFFFF0000u));
   if (wpr > 1) {
     if (lane == 0)
       for (int p = 0; p < 3; ++p) s_mx[p][warp] = mx[p];
@@ -656,25 +774,53 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G <= 2 ? 3 : 2) relu2_glu_qu
     c[p] = __fmul_rn(kQb, __frcp_rn(d[p]));
   }
   int32_t sum = 0;
+  uint32_t redo = 0u;  // chunks with codes that take the exact quotient
   const size_t at = static_cast<size_t>(active ? row : 0) * N;
-  const bool vq = (N % 16) == 0 && ((reinterpret_cast<uintptr_t>(a.qg) | reinterpret_cast<uintptr_t>(a.qu) |
-                                     reinterpret_cast<uintptr_t>(a.qh)) & 15u) == 0;
-  for_groups([&](int g, const uint32_t (&r)[16]) {
-    int8_t* const out[3] = {a.qg + at, a.qu + at, a.qh + at};
+  const bool vq = kRegs || ((N % 8) == 0 && ((reinterpret_cast<uintptr_t>(a.qg) | reinterpret_cast<uintptr_t>(a.qu) |
+                                              reinterpret_cast<uintptr_t>(a.qh)) & 7u) == 0);
+  int8_t* const out[3] = {a.qg + at, a.qu + at, a.qh + at};
+  auto values = [&](int p, const uint32_t (&r)[2][4], float2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = bf16_2(p < 2 ? r[p][i] : hword(r[0][i], r[1][i]));
+  };
+  auto exact = [&](int ch) {
+    uint32_t r[2][4];
+    load(ch, r);
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-      uint32_t r0[4], r1[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        r0[i] = p < 2 ? r[8 * p + i] : hword(r[i], r[8 + i]);
-        r1[i] = p < 2 ? r[8 * p + 4 + i] : hword(r[4 + i], r[12 + i]);
+      float2 f[4];
+      values(p, r, f);
+      float emax = 0.0f;
+      const uint2 w0 = codes8_near(f, c[p], emax);
+      if (emax > kCodesNear) {
+        const uint2 w = codes8_exact(f, d[p]);
+        store8_codes(out[p], 8 * ch, N, vq, w);
+        if (p == 2) sum += code_sum(w) - code_sum(w0);
       }
-      int32_t sm = 0;
-      const uint4 w = group_codes<false>(r0, r1, c[p], d[p], sm);
-      if (p == 2) sum += sm;
-      store16_codes(out[p], 16 * g, N, vq, w);
+    }
+  };
+  for_chunks([&](int j, int ch, const uint32_t (&r)[2][4]) {
+    float emax = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      float2 f[4];
+      values(p, r, f);
+      const uint2 w = codes8_near(f, c[p], emax);
+      if (p == 2) sum += code_sum(w);
+      store8_codes(out[p], 8 * ch, N, vq, w);
+    }
+    if (emax > kCodesNear) {
+      if (kRegs)
+        redo |= 1u << j;
+      else
+        exact(ch);
     }
   });
+  while (kRegs && redo) {
+    const int j = __ffs(redo) - 1;
+    redo &= redo - 1;
+    exact(c0 + j * cstride);
+  }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (wpr > 1) {
     if (lane == 0) s_sum[warp] = sum;
@@ -716,22 +862,19 @@ __global__ void __launch_bounds__(256) relu2_glu_backward_kernel(
     uint32_t og[8], ou[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float fg[4], fu[4], a[4], b[4];
+      float2 fg[2], fu[2];
       codes4_f32(wg[i], fg);
       codes4_f32(wu[i], fu);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t hw = i < 2 ? h0[2 * i + (e >> 1)] : h1[2 * (i - 2) + (e >> 1)];
-        const float d = (e & 1) ? bf16_hi(hw) : bf16_lo(hw);
-        const float rp = fmaxf(__fmul_rn(fg[e], sg), 0.0f);
-        const float dr = d * rp;
-        a[e] = 2.0f * dr * __fmul_rn(fu[e], su);
-        b[e] = dr * rp;
+      for (int h = 0; h < 2; ++h) {
+        const float2 d = bf16_2(i < 2 ? h0[2 * i + h] : h1[2 * (i - 2) + h]);
+        float2 rp = __fmul2_rn(fg[h], splat2(sg));
+        rp = make_float2(fmaxf(rp.x, 0.0f), fmaxf(rp.y, 0.0f));
+        const float2 dr = __fmul2_rn(d, rp);
+        const float2 p = __fmul2_rn(__fadd2_rn(dr, dr), __fmul2_rn(fu[h], splat2(su))), q = __fmul2_rn(dr, rp);
+        og[2 * i + h] = pack_bf16x2(p.x, p.y);
+        ou[2 * i + h] = pack_bf16x2(q.x, q.y);
       }
-      og[2 * i] = pack_bf16x2(a[0], a[1]);
-      og[2 * i + 1] = pack_bf16x2(a[2], a[3]);
-      ou[2 * i] = pack_bf16x2(b[0], b[1]);
-      ou[2 * i + 1] = pack_bf16x2(b[2], b[3]);
     }
     store8_bf16(dg + at, k0, N, vo, og);
     store8_bf16(dg + at, k0 + 8, N, vo, og + 4);
