@@ -2,7 +2,7 @@
 // (include/bitlinear.h, section "Training"): argument checks, launch shapes and
 // launches.  Part of the library's one translation unit.
 #pragma once
-#include "train_gemm.cuh"
+#include "train_few.cuh"
 
 namespace bl {
 namespace {
@@ -145,6 +145,12 @@ bitlinear_status check_norm_backward(const NbArgs& a, const float* dw, const flo
   return BITLINEAR_OK;
 }
 
+bitlinear_status dequant_launch(const int8_t* q, int64_t ldq, const float* gamma, int M, int K, uint16_t* y,
+                                int64_t ldy, cudaStream_t s, bool pdl, int sm_count) {
+  const int lanes = row_lanes(M, K, 8, sm_count), rpc = 256 / lanes;
+  return launch(dequant_act_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, s, pdl, q, ldq, gamma, M, K, y, ldy, lanes);
+}
+
 // ---------------------------------------------------------------- gradient products
 // How a product's 256 x 256 tiles are given to the pairs: whole rounds of
 // tiles over their whole reduction, the tiles left over cut into `split` parts.
@@ -191,7 +197,35 @@ size_t gg_slab_bytes(const GgPlan& p) {
   return static_cast<size_t>(p.units - p.full) * kGgSlab * 4;
 }
 
-// Workspace: slabs | dy with padded rows | codes with padded rows or expanded N:M weights.
+// Whether a product restores its compressed operand (`elems` elements) to bf16 before it starts: where what its
+// k-blocks save (us each, against expanding in place) exceeds the extra pass, a launch and `bytes` of traffic an
+// element at 6 TB/s.
+bool gg_dense(const GgPlan& p, double save_us, int64_t elems, double bytes) {
+  const int64_t rounds = (p.full + p.pairs - 1) / p.pairs;
+  const int64_t left = p.units - p.full;
+  const double kblocks = static_cast<double>(rounds) * p.kblocks + static_cast<double>((left + p.pairs - 1) / p.pairs) * p.per;
+  return kblocks * save_us > 2.5 + static_cast<double>(elems) * bytes / 6e6;
+}
+
+// Few-token products take train_few.cuh: up to 32 tokens, or while its CTAs, one for 16 tokens and half a span of
+// columns, fit the SMs once.  Measured (us, few / pair GEMM): 16 tokens, N = 2560, K = 6912: 7.8 / 18.0; 32: 14.1 /
+// 19.3; 64: 20.7 / 19.9.  N = 11008, K = 2048, 64 tokens (128 CTAs): 21.5 / 25.6; 96: 40 / 26.
+bool few_tokens(int M, int K, int sm_count) {
+  const int64_t groups = 2 * ((K + kFewSpan - 1) / kFewSpan);
+  return M <= 32 || groups * ((M + 15) / 16) <= sm_count;
+}
+
+bitlinear_status few_launch(FewArgs a, cudaStream_t s, int sm_count) {
+  const int groups = 2 * ((a.K + kFewSpan - 1) / kFewSpan), mt = (a.M + 15) / 16;
+  a.chunks = (a.N + kFewRed - 1) / kFewRed;
+  // parts of N: while the CTAs fit the SMs and each warp keeps a piece of its own
+  a.cs = 1;
+  while (a.cs < 8 && 2 * a.cs * groups * mt <= sm_count && 2 * a.cs * kFewWarps <= a.chunks) a.cs *= 2;
+  a.per = (a.chunks + a.cs - 1) / a.cs;
+  return launch_ex(few_input_kernel, dim3(groups * a.cs, mt), dim3(32 * kFewWarps), kFewSmem, s, true, a.cs, a);
+}
+
+// Workspace: slabs | dy with padded rows | B: codes with padded rows, expanded N:M codes, or bf16 values.
 struct GgLayout {
   size_t dy, b, total;  // offsets of the second and third part, whole size
   int64_t lddy;         // row stride of dy that TMA reads, in elements
@@ -204,6 +238,16 @@ GgLayout gg_layout(const GgPlan& p, int64_t M, int64_t N, int64_t lddy, size_t b
   l.b = l.dy + (pad ? align256(static_cast<size_t>(M) * l.lddy * 2) : 0);
   l.total = l.b + align256(b_bytes);
   return l;
+}
+
+bool bw_dense(const GgPlan& p, int64_t M, int K) { return gg_dense(p, 0.14, M * K, 3.0); }
+bool bi_dense(const GgPlan& p, int64_t N, int K) { return gg_dense(p, 0.06, N * K, 2.25); }
+size_t bw_b_bytes(const GgPlan& p, int64_t M, int K, int64_t ldq) {
+  return bw_dense(p, M, K) ? static_cast<size_t>(M) * k16(K) * 2 : ldq % 16 ? static_cast<size_t>(M) * k16(K) : 0;
+}
+size_t bi_few_bytes(int N, int K, int nm_m) { return nm_m ? static_cast<size_t>(N) * dense_ld(K) : 0; }
+size_t bi_b_bytes(const GgPlan& p, int N, int K, int nm_m) {
+  return bi_dense(p, N, K) ? static_cast<size_t>(N) * k16(K) * 2 : nm_m ? static_cast<size_t>(N) * dense_ld(K) : 0;
 }
 
 // Puts dy's rows where TMA can step them, if they are not.
@@ -219,12 +263,35 @@ bitlinear_status gg_dy(const uint16_t** dy, int64_t lddy, int M, int N, uint8_t*
 
 template <bool kWeight>
 bitlinear_status gg_launch(const CUtensorMap& mA, const CUtensorMap& mB, const GradArgs& a, const GgPlan& p,
-                           cudaStream_t s) {
-  bitlinear_status st = launch_ex(grad_gemm_kernel<kWeight>, dim3(2 * p.pairs), dim3(kGgThreads), GG<kWeight>::SMEM, s,
-                                  true, 2, mA, mB, a);
+                           bool dense, cudaStream_t s) {
+  auto go = [&](auto kern, int threads, size_t smem) {
+    return launch_ex(kern, dim3(2 * p.pairs), dim3(threads), smem, s, true, 2, mA, mB, a);
+  };
+  bitlinear_status st = dense ? go(grad_gemm_kernel<kWeight, true>, GG<kWeight, true>::THREADS, GG<kWeight, true>::SMEM)
+                              : go(grad_gemm_kernel<kWeight, false>, GG<kWeight, false>::THREADS,
+                                   GG<kWeight, false>::SMEM);
   if (st != BITLINEAR_OK || p.units == p.full) return st;
   const int tiles = p.row_tiles * p.col_tiles - p.full;
   return launch(grad_reduce_kernel<kWeight>, dim3(8 * tiles), dim3(256), 0, s, true, a);
+}
+
+// The packed rows as dense codes, or as bf16 values, in `out`.
+bitlinear_status bi_expand(const bitlinear_weights* w, uint8_t* out, bool bf16, bool pdl, cudaStream_t s) {
+  ExpandArgs e;
+  e.codes = w->codes;
+  e.meta = w->meta;
+  const bitlinear_status st = bitlinear_packed_layout(w->N, w->K, w->nm_n, w->nm_m, &e.ldc, &e.ldm, nullptr, nullptr);
+  if (st != BITLINEAR_OK) return st;
+  e.ldd = bf16 ? k16(w->K) : dense_ld(w->K);
+  e.N = w->N;
+  e.K = w->K;
+  e.nm_n = w->nm_n;
+  e.nm_m = w->nm_m;
+  e.out = reinterpret_cast<uint32_t*>(out);
+  const int64_t words = static_cast<int64_t>(w->N) * (e.ldd / (bf16 ? 16 : 4));
+  const dim3 grid(static_cast<unsigned>((words + 255) / 256));
+  return bf16 ? launch(ternary_bf16_kernel, grid, dim3(256), 0, s, pdl, e)
+              : launch(nm_expand_kernel, grid, dim3(256), 0, s, pdl, e);
 }
 
 void gg_args(GradArgs* a, const GgPlan& p, int rows, int cols, int red, void* ws, DeviceState* dev) {
@@ -241,9 +308,6 @@ void gg_args(GradArgs* a, const GgPlan& p, int rows, int cols, int red, void* ws
   a->slab = static_cast<float*>(ws);
   a->status = dev->status;
 }
-
-size_t bw_codes_bytes(int64_t M, int K, int64_t ldq) { return ldq % 16 ? static_cast<size_t>(M) * k16(K) : 0; }
-size_t bi_codes_bytes(int N, int K, int nm_m) { return nm_m ? static_cast<size_t>(N) * dense_ld(K) : 0; }
 
 }  // namespace
 }  // namespace bl
@@ -376,9 +440,7 @@ bitlinear_status bitlinear_dequant_act(const int8_t* q, int64_t ldq, const float
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
-  const int lanes = row_lanes(M, K, 8, dev->sm_count), rpc = 256 / lanes;
-  st = launch(dequant_act_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, static_cast<cudaStream_t>(stream), false, q,
-              ldq, gamma, M, K, y, lanes);
+  st = dequant_launch(q, ldq, gamma, M, K, y, K, static_cast<cudaStream_t>(stream), false, dev->sm_count);
   if (st == BITLINEAR_OK) t_last_kernel = "dequant_act";
   return st;
 }
@@ -452,7 +514,8 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
 
 size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq) {
   if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || ldq < K) return 0;
-  return gg_layout(gg_plan(N, K, M, plan_sm_count()), M, N, lddy, bw_codes_bytes(M, K, ldq)).total;
+  const GgPlan p = gg_plan(N, K, M, plan_sm_count());
+  return gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq)).total;
 }
 
 bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, const int8_t* q, int64_t ldq,
@@ -471,22 +534,27 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   if (st != BITLINEAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const GgPlan p = gg_plan(N, K, M, dev->sm_count);
-  const GgLayout l = gg_layout(p, M, N, lddy, bw_codes_bytes(M, K, ldq));
+  const GgLayout l = gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq));
   if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);
   if (st != BITLINEAR_OK) return st;
-  if (ldq % 16) {
+  const bool dense = bw_dense(p, M, K);
+  if (dense) {
+    st = dequant_launch(q, ldq, gamma, M, K, reinterpret_cast<uint16_t*>(ws + l.b), k16(K), s, true, dev->sm_count);
+  } else if (ldq % 16) {
     int8_t* d = reinterpret_cast<int8_t*>(ws + l.b);
     st = launch(pad_rows_kernel<int8_t>, dim3(std::min(M, 16 * dev->sm_count)), dim3(256), 0, s, true, q, ldq,
                 static_cast<int64_t>(M), K, d, k16(K));
-    if (st != BITLINEAR_OK) return st;
     q = d;
     ldq = k16(K);
   }
+  if (st != BITLINEAR_OK) return st;
   CUtensorMap mA, mB;
   if (!make_map_u8(&mA, dy, 2 * static_cast<uint64_t>(N), M, 2 * static_cast<uint64_t>(l.lddy), 128, kGgRed, 128) ||
-      !make_map_u8(&mB, q, K, M, static_cast<uint64_t>(ldq), 128, kGgRed, 0))
+      !(dense ? make_map_u8(&mB, ws + l.b, 2 * static_cast<uint64_t>(K), M, 2 * static_cast<uint64_t>(k16(K)), 128,
+                            kGgRed, 128)
+              : make_map_u8(&mB, q, K, M, static_cast<uint64_t>(ldq), 128, kGgRed, 0)))
     return BITLINEAR_ERR_CUDA;
   GradArgs a;
   gg_args(&a, p, N, K, M, workspace, dev);
@@ -494,7 +562,7 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   a.dw = dW;
   a.accumulate = (flags & BITLINEAR_FLAG_ACCUMULATE) != 0;
   a.vec = K % 8 == 0 && aligned32(dW);
-  st = gg_launch<true>(mA, mB, a, p, s);
+  st = gg_launch<true>(mA, mB, a, p, dense, s);
   if (st == BITLINEAR_OK) t_last_kernel = "backward_weight";
   return st;
 }
@@ -502,7 +570,9 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
 size_t bitlinear_backward_input_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int32_t nm_n,
                                                 int32_t nm_m) {
   if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || !pattern_ok(nm_n, nm_m)) return 0;
-  return gg_layout(gg_plan(M, K, N, plan_sm_count()), M, N, lddy, bi_codes_bytes(N, K, nm_m)).total;
+  if (few_tokens(M, K, plan_sm_count())) return bi_few_bytes(N, K, nm_m);
+  const GgPlan p = gg_plan(M, K, N, plan_sm_count());
+  return gg_layout(p, M, N, lddy, bi_b_bytes(p, N, K, nm_m)).total;
 }
 
 bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint16_t* dy, int64_t lddy, int32_t M,
@@ -518,34 +588,49 @@ bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const GgPlan p = gg_plan(M, K, N, dev->sm_count);
-  const GgLayout l = gg_layout(p, M, N, lddy, bi_codes_bytes(N, K, w->nm_m));
-  if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int64_t ld = dense_ld(K);
+  if (few_tokens(M, K, dev->sm_count)) {
+    const size_t need = bi_few_bytes(N, K, w->nm_m);
+    if (need > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < need)) return BITLINEAR_ERR_WORKSPACE;
+    FewArgs f;
+    std::memset(&f, 0, sizeof f);
+    f.codes = w->codes;
+    f.ldc = ld;
+    if (w->nm_m) {
+      st = bi_expand(w, ws, false, false, s);
+      if (st != BITLINEAR_OK) return st;
+      f.codes = ws;
+    }
+    f.N = N;
+    f.K = K;
+    f.dy = dy;
+    f.lddy = lddy;
+    f.M = M;
+    f.alpha = w->alpha;
+    f.add = add;
+    f.dx = dx;
+    st = few_launch(f, s, dev->sm_count);
+    if (st == BITLINEAR_OK) t_last_kernel = "backward_input_few";
+    return st;
+  }
+  const GgPlan p = gg_plan(M, K, N, dev->sm_count);
+  const GgLayout l = gg_layout(p, M, N, lddy, bi_b_bytes(p, N, K, w->nm_m));
+  if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);
   if (st != BITLINEAR_OK) return st;
-  const int64_t ld = dense_ld(K);
   const uint8_t* codes = w->codes;
-  if (w->nm_m) {
-    NmExpandArgs e;
-    e.codes = w->codes;
-    e.meta = w->meta;
-    st = bitlinear_packed_layout(N, K, w->nm_n, w->nm_m, &e.ldc, &e.ldm, nullptr, nullptr);
-    if (st != BITLINEAR_OK) return st;
-    e.ldd = ld;
-    e.N = N;
-    e.K = K;
-    e.nm_n = w->nm_n;
-    e.nm_m = w->nm_m;
-    e.out = reinterpret_cast<uint32_t*>(ws + l.b);
-    const int64_t words = static_cast<int64_t>(N) * (ld / 4);
-    st = launch(nm_expand_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, true, e);
+  const bool dense = bi_dense(p, N, K);
+  if (dense || w->nm_m) {
+    st = bi_expand(w, ws + l.b, dense, true, s);
     if (st != BITLINEAR_OK) return st;
     codes = ws + l.b;
   }
   CUtensorMap mA, mB;
   if (!make_map_u8(&mA, dy, 2 * static_cast<uint64_t>(N), M, 2 * static_cast<uint64_t>(l.lddy), 128, 128, 128) ||
-      !make_map_u8(&mB, codes, static_cast<uint64_t>(ld), N, static_cast<uint64_t>(ld), 32, kGgRed, 0))
+      !(dense ? make_map_u8(&mB, codes, 2 * static_cast<uint64_t>(K), N, 2 * static_cast<uint64_t>(k16(K)), 128, kGgRed,
+                            128)
+              : make_map_u8(&mB, codes, static_cast<uint64_t>(ld), N, static_cast<uint64_t>(ld), 32, kGgRed, 0)))
     return BITLINEAR_ERR_CUDA;
   GradArgs a;
   gg_args(&a, p, M, K, N, workspace, dev);
@@ -553,7 +638,7 @@ bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint
   a.add = add;
   a.dx = dx;
   a.vec = K % 16 == 0 && aligned32(dx) && aligned32(add);
-  st = gg_launch<false>(mA, mB, a, p, s);
+  st = gg_launch<false>(mA, mB, a, p, dense, s);
   if (st == BITLINEAR_OK) t_last_kernel = "backward_input";
   return st;
 }

@@ -20,6 +20,11 @@
 // token's scale, which cannot leave the sum over tokens; that rounding to bf16
 // is the restored activation's own type (dequant_act gives the same values).
 //
+// Expanding costs the MMAs' shared-memory bandwidth (a k-block of 256 x 256 x 64
+// takes 0.43 us with 2-bit rows and 0.53 with 8-bit codes, 0.37 without) and is
+// done again for every 256 rows of the result.  Large products therefore restore
+// B once, as bf16 in the workspace, and run with kDense (see gg_dense).
+//
 // Two CTAs of a cluster share one MMA of 256 x 256 x 16 (cta_group::2): each
 // holds its own 128 rows of A and expands its own 128 columns of B, so each
 // column is expanded once per 256 rows and the shared-memory reads per MMA
@@ -41,7 +46,7 @@ namespace bl {
 constexpr int kGgRows = 256;      // rows of a pair tile (128 a CTA)
 constexpr int kGgCols = 256;      // columns of a pair tile (128 of B a CTA)
 constexpr int kGgRed = 64;        // steps of the reduction per stage
-constexpr int kGgThreads = 512;
+constexpr int kGgGroups = 2;       // groups of four expanding warps, taking the stages in turn
 constexpr int kGgSlab = kGgRows * kGgCols;  // fp32 of one part of a split tile
 
 struct GradArgs {
@@ -62,15 +67,18 @@ struct GradArgs {
   int32_t* status;
 };
 
-template <bool kWeight>
+template <bool kWeight, bool kDense>
 struct GG {
-  static constexpr int A_STAGE = 128 * kGgRed * 2;               // 16 KB
-  static constexpr int RAW = kWeight ? kGgRed * 128 : kGgRed * 32;  // compressed rows: 128 codes, 1 or 1/4 byte each
-  static constexpr int OP = 128 * kGgRed * 2;                    // 16 KB of expanded B
-  static constexpr int S = kWeight ? 6 : 8;                      // even, like R: see gemm_tc2.cuh
-  static constexpr int R = 4;
+  static constexpr int A_STAGE = 128 * kGgRed * 2;  // 16 KB
+  static constexpr int OP = 128 * kGgRed * 2;       // 16 KB of B: [2 blocks of 64 columns][64 lines][128 B]
+  // what lands of B: the operand itself, or compressed rows of 128 codes, 1 or 1/4 byte each
+  static constexpr int RAW = kDense ? OP : kWeight ? kGgRed * 128 : kGgRed * 32;
+  static constexpr int S = kDense ? 6 : kWeight ? 6 : 8;
+  static constexpr int R = kDense ? S : 4;          // S >= R: an operand slot's wait is on the stage that filled it
+  static constexpr int GROUPS = kDense ? 0 : kGgGroups;
+  static constexpr int THREADS = 32 * (8 + 4 * GROUPS);
   static constexpr int FIXED = 512;
-  static constexpr int SMEM = S * (A_STAGE + RAW) + R * OP + FIXED;
+  static constexpr int SMEM = S * (A_STAGE + RAW) + (kDense ? 0 : R * OP) + FIXED;
   static constexpr uint32_t IDESC = idesc_bf16(kGgRows, kGgCols, kWeight, true);
   static_assert(SMEM <= kTcSmemMax, "shared memory");
   static_assert(RAW % 1024 == 0, "stages keep the swizzle's alignment");
@@ -155,13 +163,14 @@ __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int
 }
 
 // mapA: dy; box 128 bytes x 128 rows (dx) or 128 bytes x 64 rows (dW), landed 128-byte-swizzled.
-// mapB: the compressed rows; box 32 bytes (2-bit) or 128 bytes (8-bit) x 64 rows, landed as they are.
-template <bool kWeight>
-__global__ void __launch_bounds__(kGgThreads, 1)
+// mapB: the compressed rows; box 32 bytes (2-bit) or 128 bytes (8-bit) x 64 rows, landed as they are; with kDense the
+// bf16 rows, box 128 bytes x 64 rows, landed 128-byte-swizzled.
+template <bool kWeight, bool kDense>
+__global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     grad_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                      const GradArgs a) {
-  using C = GG<kWeight>;
-  constexpr int S = C::S, R = C::R;
+  using C = GG<kWeight, kDense>;
+  constexpr int S = C::S, R = C::R, G = C::GROUPS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // both CTAs see the same offset, so both leave here together (before any cluster barrier)
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
@@ -169,11 +178,11 @@ __global__ void __launch_bounds__(kGgThreads, 1)
     return;
   }
   uint8_t* sA = smem_raw;                   // [S][16 KB]
-  uint8_t* sOp = sA + S * C::A_STAGE;       // [R][2 blocks of 64 columns][64 lines][128 B]
-  uint8_t* sRaw = sOp + R * C::OP;          // [S][RAW]
+  uint8_t* sOp = sA + S * C::A_STAGE;       // [R][OP]
+  uint8_t* sRaw = sOp + (kDense ? 0 : R * C::OP);  // [S][RAW]; kDense: the operand slots themselves
   uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + S * C::RAW);
   uint64_t* empty = full + S;
-  uint64_t* opready = empty + S;     // [R] rank 0's: both CTAs' expanding warps
+  uint64_t* opready = empty + S;     // [R] rank 0's: both CTAs' expanding warps (kDense: their forwarding threads)
   uint64_t* accfull = opready + R;   // [2]
   uint64_t* accempty = accfull + 2;  // [2] rank 0's: both CTAs' storing warps
   uint64_t* drain = accempty + 2;
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int j = 0; j < R; ++j) mbar_init(&opready[j], 8);
+    for (int j = 0; j < R; ++j) mbar_init(&opready[j], kDense ? 2 : 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
       mbar_init(&accempty[b], 8);
@@ -247,10 +256,15 @@ __global__ void __launch_bounds__(kGgThreads, 1)
           if (kWeight) {
             tma_load_2d(dA, &mapA, 2 * row0, kb * kGgRed, &full[s]);
             tma_load_2d(dA + 8192, &mapA, 2 * row0 + 128, kb * kGgRed, &full[s]);
-            tma_load_2d(sRaw + s * C::RAW, &mapB, col0, kb * kGgRed, &full[s]);
           } else {
             tma_load_2d(dA, &mapA, kb * kGgRed * 2, row0, &full[s]);
-            tma_load_2d(sRaw + s * C::RAW, &mapB, col0 / 4, kb * kGgRed, &full[s]);
+          }
+          uint8_t* dB = sRaw + s * C::RAW;
+          if (kDense) {
+            tma_load_2d(dB, &mapB, 2 * col0, kb * kGgRed, &full[s]);
+            tma_load_2d(dB + 8192, &mapB, 2 * col0 + 128, kb * kGgRed, &full[s]);
+          } else {
+            tma_load_2d(dB, &mapB, kWeight ? col0 : col0 / 4, kb * kGgRed, &full[s]);
           }
         }
       }
@@ -302,7 +316,26 @@ __global__ void __launch_bounds__(kGgThreads, 1)
         if (!mbar_wait(drain, 0)) *a.status = kDevTimeoutDrain;
       }
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (kDense && warp == 3) {
+    // -------------------------------------------------------------- both CTAs: this one's copies have landed
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      for (int g = pair; g < a.units && ok; g += npairs) {
+        int row0, col0, kb0;
+        const int n = unit_of(g, row0, col0, kb0);
+        for (int kb = 0; kb < n; ++kb, ++i) {
+          const int s = i % S;
+          if (!mbar_wait(&full[s], (i / S) & 1)) {
+            *a.status = kDevTimeoutUnpack;
+            ok = false;
+            break;
+          }
+          mbar_arrive_remote_cta(opready0 + static_cast<uint32_t>(s * 8));
+        }
+      }
+    }
+  } else if (!kDense && warp >= 4 && warp < 4 + 4 * G) {
     // -------------------------------------------------------------- expansion (both CTAs)
     // Eight lanes take a line's 128 columns, 16 each; lanes 4 .. 7 (the second
     // block of 64) store their odd chunk first, so the eight 16-byte stores of a
@@ -317,7 +350,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
       int row0, col0, kb0;
       const int n = unit_of(g, row0, col0, kb0);
       for (int kb = kb0; kb < kb0 + n; ++kb, ++i) {
-        if ((i & 1) != grp) continue;
+        if (i % kGgGroups != grp) continue;
         const int s = i % S, j = i % R;
         float sc[4];
         if (kWeight) {  // the tokens' scales, read while the copy is in flight
@@ -367,9 +400,9 @@ __global__ void __launch_bounds__(kGgThreads, 1)
         if (lane == 0) mbar_arrive_remote_cta(opready0 + static_cast<uint32_t>(j * 8));
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + 4 * G) {
     // -------------------------------------------------------------- stores (both CTAs, own rows)
-    const int q = warp - 12;
+    const int q = warp - 4 - 4 * G;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float alpha = kWeight ? 1.0f : *a.alpha;
     int t = 0;
@@ -390,8 +423,8 @@ __global__ void __launch_bounds__(kGgThreads, 1)
         tc_wait_ld();
         float v[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c)  // dx: accumulator column 2 i + h of a 16-group is output column i + 8 h
-          v[kWeight ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
+        for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
+          v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
         if (g >= a.full && a.split > 1) {
           float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + lrow * kGgCols + c0;
 #pragma unroll
@@ -456,45 +489,79 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const T* __restrict__ src
 
 // N:M rows expanded to dense codes (16 weights a thread), the layout of the
 // dense matrix of the same size; positions past K hold code 1.
-struct NmExpandArgs {
+struct ExpandArgs {
   const uint8_t* codes;
   const uint8_t* meta;
-  int64_t ldc, ldm, ldd;
+  int64_t ldc, ldm, ldd;  // ldd: row stride of the dense codes, bytes (bf16: of the values, elements)
   int N, K, nm_n, nm_m;
   uint32_t* out;
 };
-__global__ void __launch_bounds__(256) nm_expand_kernel(const NmExpandArgs a) {
+
+// The 16 dense codes from k0 (a multiple of 16) of row n of an N:M matrix.  K is a multiple of m, so the 16 lie in
+// whole blocks; positions past K get code 1 (a row's bytes end with zeros, which name no kept position of 1:8 ..
+// 7:8 and are masked for 2:4).
+__device__ __forceinline__ uint32_t nm_codes16(const ExpandArgs& a, int64_t n, int k0) {
+  const int w = k0 >> 4;
+  const uint32_t mt = *reinterpret_cast<const uint16_t*>(a.meta + n * a.ldm + 2 * w);  // 4 nibbles, or 2 masks
+  uint32_t o = 0x55555555u;
+  if (a.nm_m == 4) {
+    const uint32_t c = *reinterpret_cast<const uint16_t*>(a.codes + n * a.ldc + 2 * w);  // 8 kept codes
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t s0 = 8 * b + 2 * ((mt >> (4 * b)) & 3u), s1 = 8 * b + 2 * ((mt >> (4 * b + 2)) & 3u);
+      // code 1 (01) is there: its place becomes c by flipping c ^ 1
+      if (k0 + 4 * b < a.K) o ^= ((((c >> (4 * b)) & 3u) ^ 1u) << s0) ^ ((((c >> (4 * b + 2)) & 3u) ^ 1u) << s1);
+    }
+  } else {
+    const int bits = 4 * a.nm_n;  // kept codes of two blocks
+    const uint8_t* p = a.codes + n * a.ldc + ((w * bits) >> 3);
+    const int shift = (w * bits) & 7;
+    uint64_t v = 0;
+    for (int i = 0; 8 * i < bits + shift; ++i) v |= static_cast<uint64_t>(p[i]) << (8 * i);
+    uint32_t c = static_cast<uint32_t>(v >> shift);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t kept = c >> (2 * a.nm_n * b);
+      if (k0 + 8 * b < a.K)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((mt >> (8 * b + j)) & 1u) {
+            o ^= ((kept & 3u) ^ 1u) << (16 * b + 2 * j);
+            kept >>= 2;
+          }
+    }
+  }
+  return o;
+}
+
+__global__ void __launch_bounds__(256) nm_expand_kernel(const ExpandArgs a) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int words = static_cast<int>(a.ldd / 4);
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (at >= static_cast<int64_t>(a.N) * words) return;
   const int64_t n = at / words;
-  const int k0 = static_cast<int>(at - n * words) * 16;
-  const uint8_t* c = a.codes + n * a.ldc;
-  const uint8_t* mt = a.meta + n * a.ldm;
-  uint32_t o = 0x55555555u;
-  auto kept = [&](int pos) { return static_cast<uint32_t>(c[pos >> 2] >> (2 * (pos & 3))) & 3u; };
-  if (a.nm_m == 4) {
-    for (int b = k0 / 4; b < k0 / 4 + 4 && 4 * b < a.K; ++b) {
-      const uint32_t nib = mt[b >> 1] >> (4 * (b & 1));
-      const int s0 = 2 * (4 * b - k0 + static_cast<int>(nib & 3u)), s1 = 2 * (4 * b - k0 + static_cast<int>((nib >> 2) & 3u));
-      o = (o & ~(3u << s0)) | (kept(2 * b) << s0);
-      o = (o & ~(3u << s1)) | (kept(2 * b + 1) << s1);
-    }
-  } else {
-    for (int b = k0 / 8; b < k0 / 8 + 2 && 8 * b < a.K; ++b) {
-      const uint32_t mask = mt[b];
-      int pos = b * a.nm_n;
-      for (int j = 0; j < 8; ++j)
-        if ((mask >> j) & 1u) {
-          const int sh = 2 * (8 * b - k0 + j);
-          if (pos < (b + 1) * a.nm_n) o = (o & ~(3u << sh)) | (kept(pos) << sh);
-          ++pos;
-        }
-    }
+  a.out[at] = nm_codes16(a, n, static_cast<int>(at - n * words) * 16);
+}
+
+// Dense or N:M rows as bf16 values, rows of a multiple of 16 columns (those past K are never read).
+__global__ void __launch_bounds__(256) ternary_bf16_kernel(const ExpandArgs a) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int words = static_cast<int>(a.ldd / 16);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= static_cast<int64_t>(a.N) * words) return;
+  const int64_t n = at / words;
+  const int w = static_cast<int>(at - n * words);
+  const uint32_t c = a.nm_m ? nm_codes16(a, n, 16 * w) : *reinterpret_cast<const uint32_t*>(a.codes + n * a.ldc + 4 * w);
+  uint32_t v[8], o[8];
+  ternary16_bf16(c, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x5410);
+    o[4 + i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x7632);
   }
-  a.out[at] = o;
+  st_global_v8(reinterpret_cast<uint16_t*>(a.out) + at * 16, o);
 }
 
 }  // namespace bl

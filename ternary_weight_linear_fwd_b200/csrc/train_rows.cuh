@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 // threads takes 256 / lanes rows, `lanes` threads a row, 16 codes each a step.
 __global__ void __launch_bounds__(256) dequant_act_kernel(const int8_t* __restrict__ q, int64_t ldq,
                                                           const float* __restrict__ gamma, int M, int K,
-                                                          uint16_t* __restrict__ y, int lanes) {
+                                                          uint16_t* __restrict__ y, int64_t ldy, int lanes) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int r = threadIdx.x / lanes, t = threadIdx.x - r * lanes;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const int8_t* __restri
   if (row >= M) return;
   const float s = __fdiv_rn(gamma[row], kQb);
   const bool qv = (ldq % 16) == 0 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
-  const bool yv = (K % 8) == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
+  const bool yv = (ldy % 8) == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
   for (int k0 = 16 * t; k0 < K; k0 += 16 * lanes) {
     uint32_t w[4], o[8];
     load16_codes(q + row * ldq, k0, K, qv, w);
@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const int8_t* __restri
         o[2 * i + h] = pack_bf16x2(f[h].x, f[h].y);
       }
     }
-    store8_bf16(y + row * K, k0, K, yv, o);
-    store8_bf16(y + row * K, k0 + 8, K, yv, o + 4);
+    store8_bf16(y + row * ldy, k0, K, yv, o);
+    store8_bf16(y + row * ldy, k0 + 8, K, yv, o + 4);
   }
 }
 

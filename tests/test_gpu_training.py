@@ -628,3 +628,33 @@ def test_refusals():
               lambda: bl.backward_weight(dy[:0], q[:0], gamma[:0]), lambda: bl.backward_input(pw, dy[:0])):
         with pytest.raises(bl.BitLinearError):
             f()
+
+
+# ---------------------------------------------------------------- products large enough to restore an operand first
+@pytest.mark.parametrize("M,N,K", [(4096, 2600, 2100), (2200, 6912, 2563), (8000, 1300, 1500)])
+def test_backward_weight_restored_operand(M, N, K):
+    dy = _rand(M + N, M, N, scale=1e-3)
+    dy[-M // 8:] = 0
+    q, gamma = _checkpoint(M + K, M, K)
+    x = _values(q, gamma).to(BF)
+    want, size = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+    dW = bl.backward_weight(dy, q, gamma)
+    _close(dW, want, 2 * (M + 16) * U * size, "dW")
+    # a strided checkpoint of odd width, and a second run, give the same bits
+    assert torch.equal(dW, bl.backward_weight(_strided(dy, 8), _strided(q, 13), gamma))
+    out = torch.ones(N, K, device=DEV)
+    bl.backward_weight(dy, q, gamma, out=out, accumulate=True)
+    _close(out, want + 1, 2 * (M + 16) * U * size + 2 * (M // 256 + 2) * U * (1 + size), "dW accumulated")
+
+
+@pytest.mark.parametrize("n,m", [(0, 0), (2, 4), (3, 8)])
+@pytest.mark.parametrize("M,N,K", [(4100, 8200, 2056), (16000, 1000, 2568)])
+def test_backward_input_restored_operand(n, m, M, N, K):
+    W = 0.02 * torch.randn(N, K, device=DEV, generator=_gen(n * m))
+    w = bl.pack_weights(W, n, m)
+    T = torch.round(W / (w.alpha + 1e-5)).clamp(-1, 1)
+    if m:
+        blocks = W.view(N, K // m, m)
+        T *= torch.zeros_like(blocks).scatter_(2, blocks.abs().argsort(dim=2, descending=True, stable=True)[:, :, :n],
+                                               1).view(N, K)
+    _check_input(w, T.to(torch.int8), _rand(M + N, M, N, scale=1e-3), _rand(M, M, K, scale=1e-3))
