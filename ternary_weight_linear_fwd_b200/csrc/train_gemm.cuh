@@ -103,11 +103,28 @@ __device__ __forceinline__ void ternary16_bf16(uint32_t w, uint32_t (&o)[8]) {
   }
 }
 
+// What is added to one thread's 32 columns of dx (bf16 pairs), or to dW (fp32), where they are whole; loaded ahead of
+// the sums.
+template <bool kWeight>
+__device__ __forceinline__ void grad_addend32(const GradArgs& a, int64_t row, int col, uint32_t (&s)[kWeight ? 32 : 16]) {
+  if (!(a.vec && col + 32 <= a.cols && row < a.rows)) return;
+  const int64_t at = row * a.cols + col;
+  if (kWeight) {
+    if (a.accumulate)
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) ld_global_v8(a.dw + at + i, s + i);
+  } else {
+    if (a.add)
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) ld_global_v8(a.add + at + i, s + i / 2);
+  }
+}
+
 // Stores one thread's 32 consecutive columns (from col) of output row `row`,
-// fp32 sums v in natural column order.
+// fp32 sums v in natural column order; s: grad_addend32's.
 template <bool kWeight>
 __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int col, const float (&v)[32],
-                                             float alpha) {
+                                             const uint32_t (&s)[kWeight ? 32 : 16], float alpha) {
   const int64_t at = row * a.cols + col;
   const bool whole = a.vec && col + 32 <= a.cols;
   if (kWeight) {
@@ -116,14 +133,9 @@ __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         uint32_t o[8];
-        if (a.accumulate) {
-          ld_global_v8(p + i, o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__fadd_rn(__uint_as_float(o[e]), v[i + e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(v[i + e]);
-        }
+        for (int e = 0; e < 8; ++e)
+          o[e] = __float_as_uint(a.accumulate ? __fadd_rn(__uint_as_float(s[i + e]), v[i + e]) : v[i + e]);
         st_global_v8(p + i, o);
       }
     } else {
@@ -137,14 +149,13 @@ __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int
     if (whole) {
 #pragma unroll
       for (int i = 0; i < 32; i += 16) {
-        uint32_t o[8], s[8];
-        if (q) ld_global_v8(q + i, s);
+        uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float lo = __fmul_rn(v[i + 2 * e], alpha), hi = __fmul_rn(v[i + 2 * e + 1], alpha);
           if (q) {
-            lo = __fadd_rn(lo, bf16_lo(s[e]));
-            hi = __fadd_rn(hi, bf16_hi(s[e]));
+            lo = __fadd_rn(lo, bf16_lo(s[i / 2 + e]));
+            hi = __fadd_rn(hi, bf16_hi(s[i / 2 + e]));
           }
           o[e] = pack_bf16x2(lo, hi);
         }
@@ -411,6 +422,10 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       int row0, col0, kb0;
       unit_of(g, row0, col0, kb0);
       const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
+      const bool part = g >= a.full && a.split > 1;
+      constexpr int kAdd = kWeight ? 32 : 16;
+      uint32_t s0[kAdd];
+      if (!part) grad_addend32<kWeight>(a, row0 + lrow, col0, s0);
       if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
         *a.status = kDevTimeoutEpilogue;
         break;
@@ -418,20 +433,23 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < kGgCols; c0 += 32) {
-        uint32_t w[32];
+        uint32_t w[32], s1[kAdd];
         tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
+        if (!part && c0 + 32 < kGgCols) grad_addend32<kWeight>(a, row0 + lrow, col0 + c0 + 32, s1);
         tc_wait_ld();
         float v[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
           v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
-        if (g >= a.full && a.split > 1) {
+        if (part) {
           float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + lrow * kGgCols + c0;
 #pragma unroll
           for (int c = 0; c < 32; c += 8) st_global_v8(p + c, reinterpret_cast<const uint32_t*>(v + c));
         } else if (row0 + lrow < a.rows && col0 + c0 < a.cols) {
-          grad_store32<kWeight>(a, row0 + lrow, col0 + c0, v, alpha);
+          grad_store32<kWeight>(a, row0 + lrow, col0 + c0, v, s0, alpha);
         }
+#pragma unroll
+        for (int i = 0; i < kAdd; ++i) s0[i] = s1[i];
       }
       tc_fence_before();
       __syncwarp();
@@ -463,6 +481,8 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
   const int col = (tile - rt * a.col_tiles) * kGgCols + lc;
   if (row >= a.rows || col >= a.cols) return;
   const float* p = a.slab + static_cast<size_t>(unit) * a.split * kGgSlab + lrow * kGgCols + lc;
+  uint32_t add[kWeight ? 32 : 16];
+  grad_addend32<kWeight>(a, row, col, add);
   float v[32];
 #pragma unroll
   for (int c = 0; c < 32; ++c) v[c] = 0.0f;
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
 #pragma unroll
     for (int c = 0; c < 32; ++c) v[c] = __fadd_rn(v[c], __uint_as_float(w[c]));
   }
-  grad_store32<kWeight>(a, row, col, v, kWeight ? 1.0f : *a.alpha);
+  grad_store32<kWeight>(a, row, col, v, add, kWeight ? 1.0f : *a.alpha);
 }
 
 // ----------------------------------------------------------------- operands put in order
