@@ -272,7 +272,7 @@ bitlinear_status gg_launch(const CUtensorMap& mA, const CUtensorMap& mB, const G
                                    GG<kWeight, false>::SMEM);
   if (st != BITLINEAR_OK || p.units == p.full) return st;
   const int tiles = p.row_tiles * p.col_tiles - p.full;
-  return launch(grad_reduce_kernel<kWeight>, dim3(8 * tiles), dim3(256), 0, s, true, a);
+  return launch(grad_reduce_kernel<kWeight>, dim3(kGgReduceCtas * tiles), dim3(256), 0, s, true, a);
 }
 
 // The packed rows as dense codes, or as bf16 values, in `out`.

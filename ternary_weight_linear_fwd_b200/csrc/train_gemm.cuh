@@ -63,7 +63,7 @@ struct GradArgs {
   float* dw;              // dW: fp32 [rows, cols]
   int accumulate;         // dW: add to it
   int vec;                // output (and add) rows are 32-byte aligned
-  float* slab;            // [(tiles - full) * split][256][256]
+  float* slab;            // [(tiles - full) * split][32 groups of 8 columns][256 rows][8]: a warp's store is contiguous
   int32_t* status;
 };
 
@@ -103,35 +103,35 @@ __device__ __forceinline__ void ternary16_bf16(uint32_t w, uint32_t (&o)[8]) {
   }
 }
 
-// What is added to one thread's 32 columns of dx (bf16 pairs), or to dW (fp32), where they are whole; loaded ahead of
+// What is added to one thread's W columns of dx (bf16 pairs), or to dW (fp32), where they are whole; loaded ahead of
 // the sums.
-template <bool kWeight>
-__device__ __forceinline__ void grad_addend32(const GradArgs& a, int64_t row, int col, uint32_t (&s)[kWeight ? 32 : 16]) {
-  if (!(a.vec && col + 32 <= a.cols && row < a.rows)) return;
+template <bool kWeight, int W>
+__device__ __forceinline__ void grad_addend(const GradArgs& a, int64_t row, int col, uint32_t (&s)[kWeight ? W : W / 2]) {
+  if (!(a.vec && col + W <= a.cols && row < a.rows)) return;
   const int64_t at = row * a.cols + col;
   if (kWeight) {
     if (a.accumulate)
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) ld_global_v8(a.dw + at + i, s + i);
+      for (int i = 0; i < W; i += 8) ld_global_v8(a.dw + at + i, s + i);
   } else {
     if (a.add)
 #pragma unroll
-      for (int i = 0; i < 32; i += 16) ld_global_v8(a.add + at + i, s + i / 2);
+      for (int i = 0; i < W; i += 16) ld_global_v8(a.add + at + i, s + i / 2);
   }
 }
 
-// Stores one thread's 32 consecutive columns (from col) of output row `row`,
-// fp32 sums v in natural column order; s: grad_addend32's.
-template <bool kWeight>
-__device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int col, const float (&v)[32],
-                                             const uint32_t (&s)[kWeight ? 32 : 16], float alpha) {
+// Stores one thread's W consecutive columns (from col) of output row `row`,
+// fp32 sums v in natural column order; s: grad_addend's.
+template <bool kWeight, int W>
+__device__ __forceinline__ void grad_store(const GradArgs& a, int64_t row, int col, const float (&v)[W],
+                                           const uint32_t (&s)[kWeight ? W : W / 2], float alpha) {
   const int64_t at = row * a.cols + col;
-  const bool whole = a.vec && col + 32 <= a.cols;
+  const bool whole = a.vec && col + W <= a.cols;
   if (kWeight) {
     float* p = a.dw + at;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
+      for (int i = 0; i < W; i += 8) {
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -140,7 +140,7 @@ __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < W; ++i)
         if (col + i < a.cols) p[i] = a.accumulate ? __fadd_rn(p[i], v[i]) : v[i];
     }
   } else {
@@ -148,7 +148,7 @@ __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int
     const uint16_t* q = a.add ? a.add + at : nullptr;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 16) {
+      for (int i = 0; i < W; i += 16) {
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -163,7 +163,7 @@ __device__ __forceinline__ void grad_store32(const GradArgs& a, int64_t row, int
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < W; ++i)
         if (col + i < a.cols) {
           float f = __fmul_rn(v[i], alpha);
           if (q) f = __fadd_rn(f, bf16_bits_to_f32(q[i]));
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       const bool part = g >= a.full && a.split > 1;
       constexpr int kAdd = kWeight ? 32 : 16;
       uint32_t s0[kAdd];
-      if (!part) grad_addend32<kWeight>(a, row0 + lrow, col0, s0);
+      if (!part) grad_addend<kWeight, 32>(a, row0 + lrow, col0, s0);
       if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
         *a.status = kDevTimeoutEpilogue;
         break;
@@ -435,18 +435,18 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       for (int c0 = 0; c0 < kGgCols; c0 += 32) {
         uint32_t w[32], s1[kAdd];
         tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
-        if (!part && c0 + 32 < kGgCols) grad_addend32<kWeight>(a, row0 + lrow, col0 + c0 + 32, s1);
+        if (!part && c0 + 32 < kGgCols) grad_addend<kWeight, 32>(a, row0 + lrow, col0 + c0 + 32, s1);
         tc_wait_ld();
         float v[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
           v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
         if (part) {
-          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + lrow * kGgCols + c0;
+          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + lrow) * 8;
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) st_global_v8(p + c, reinterpret_cast<const uint32_t*>(v + c));
+          for (int c = 0; c < 4; ++c) st_global_v8(p + c * 8 * kGgRows, reinterpret_cast<const uint32_t*>(v + 8 * c));
         } else if (row0 + lrow < a.rows && col0 + c0 < a.cols) {
-          grad_store32<kWeight>(a, row0 + lrow, col0 + c0, v, s0, alpha);
+          grad_store<kWeight, 32>(a, row0 + lrow, col0 + c0, v, s0, alpha);
         }
 #pragma unroll
         for (int i = 0; i < kAdd; ++i) s0[i] = s1[i];
@@ -467,33 +467,34 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
 }
 
 // The split tiles: adds each tile's parts in order and finishes it.  A thread
-// takes 32 columns of a row, as the storing warps do.
+// takes 16 columns of a row, four parts' loads in flight.
+constexpr int kGgReduceCtas = kGgRows * kGgCols / 16 / 256;  // of a tile
 template <bool kWeight>
 __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int unit = blockIdx.x >> 3;                                  // split tile
-  const int e = (blockIdx.x & 7) * 256 + threadIdx.x;                // 2048 (row, 32 columns) of a tile
+  const int unit = blockIdx.x / kGgReduceCtas;                              // split tile
+  const int lrow = threadIdx.x, lc = (blockIdx.x % kGgReduceCtas) * 16;     // 256 rows a CTA
   const int tile = a.full + unit;
   const int rt = tile / a.col_tiles;
-  const int lrow = e >> 3, lc = (e & 7) * 32;
   const int64_t row = static_cast<int64_t>(rt) * kGgRows + lrow;
   const int col = (tile - rt * a.col_tiles) * kGgCols + lc;
   if (row >= a.rows || col >= a.cols) return;
-  const float* p = a.slab + static_cast<size_t>(unit) * a.split * kGgSlab + lrow * kGgCols + lc;
-  uint32_t add[kWeight ? 32 : 16];
-  grad_addend32<kWeight>(a, row, col, add);
-  float v[32];
+  const float* p = a.slab + static_cast<size_t>(unit) * a.split * kGgSlab + (lc / 8 * kGgRows + lrow) * 8;
+  uint32_t add[kWeight ? 16 : 8];
+  grad_addend<kWeight, 16>(a, row, col, add);
+  float v[16];
 #pragma unroll
-  for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-  for (int s = 0; s < a.split; ++s, p += kGgSlab) {
-    uint32_t w[32];
+  for (int c = 0; c < 16; ++c) v[c] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < a.split; ++s) {
+    uint32_t w[16];
+    ld_global_v8(p + static_cast<size_t>(s) * kGgSlab, w);
+    ld_global_v8(p + static_cast<size_t>(s) * kGgSlab + 8 * kGgRows, w + 8);
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) ld_global_v8(p + c, w + c);
-#pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = __fadd_rn(v[c], __uint_as_float(w[c]));
+    for (int c = 0; c < 16; ++c) v[c] = __fadd_rn(v[c], __uint_as_float(w[c]));
   }
-  grad_store32<kWeight>(a, row, col, v, add, kWeight ? 1.0f : *a.alpha);
+  grad_store<kWeight, 16>(a, row, col, v, add, kWeight ? 1.0f : *a.alpha);
 }
 
 // ----------------------------------------------------------------- operands put in order
