@@ -158,11 +158,11 @@ struct GgPlan {
   int row_tiles, col_tiles, kblocks, full, split, per, units, pairs;
 };
 
-// Parts of the tiles left over: the fewest (rounds of pairs) x (k-blocks of a
-// part), against the cost of the slabs.  In k-blocks of 0.3 us: a part's fp32
-// tile is written in about 4 and read back by the last launch (about 10 for
-// the launch, and 1/4 per part for its bytes).
-GgPlan gg_plan(int64_t rows, int cols, int red, int sm_count) {
+// Parts of the tiles left over, by the time of their rounds: kb us a k-block (0.43 with 2-bit rows, 0.53 with 8-bit
+// codes), 0.3 a round, and once they are split 3 for the last launch and 0.04 for each part's way through memory.
+// Measured with s parts (us): dx 777 x 2560 x 640, 12 tiles of 40 k-blocks: 20.3 (s = 1), 15.4 (2), 12.5 (4, 6), 14.1
+// (8); dx 128 x 2560 x 6912, 27 of 40: 20.9, 16.2 (2), 17.8 (4); dW 2048 x 640 x 2560, 30 of 32: 23.1, 18.8 (2), 20.7 (4).
+GgPlan gg_plan(int64_t rows, int cols, int red, double kb, int sm_count) {
   GgPlan p;
   p.pairs = sm_count / 2;
   p.row_tiles = static_cast<int>((rows + kGgRows - 1) / kGgRows);
@@ -174,12 +174,12 @@ GgPlan gg_plan(int64_t rows, int cols, int red, int sm_count) {
   p.split = 1;
   p.per = p.kblocks;
   if (left > 0) {
-    int64_t best = 4ll * p.kblocks;
+    double best = p.kblocks * kb + 0.3;
     for (int s = 2; s <= 32 && 2 * s <= p.kblocks; ++s) {
       const int per = (p.kblocks + s - 1) / s;
       const int parts = (p.kblocks + per - 1) / per;
       const int64_t rounds = (static_cast<int64_t>(left) * parts + p.pairs - 1) / p.pairs;
-      const int64_t cost = 4 * rounds * (per + 4) + 40 + static_cast<int64_t>(left) * parts / 4;
+      const double cost = static_cast<double>(rounds) * (per * kb + 0.3) + 3.0 + 0.04 * left * parts;
       if (cost < best) {
         best = cost;
         p.split = parts;
@@ -514,7 +514,7 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
 
 size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq) {
   if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || ldq < K) return 0;
-  const GgPlan p = gg_plan(N, K, M, plan_sm_count());
+  const GgPlan p = gg_plan(N, K, M, 0.53, plan_sm_count());
   return gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq)).total;
 }
 
@@ -533,7 +533,7 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const GgPlan p = gg_plan(N, K, M, dev->sm_count);
+  const GgPlan p = gg_plan(N, K, M, 0.53, dev->sm_count);
   const GgLayout l = gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq));
   if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -571,7 +571,7 @@ size_t bitlinear_backward_input_workspace_bytes(int32_t M, int32_t N, int32_t K,
                                                 int32_t nm_m) {
   if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || !pattern_ok(nm_n, nm_m)) return 0;
   if (few_tokens(M, K, plan_sm_count())) return bi_few_bytes(N, K, nm_m);
-  const GgPlan p = gg_plan(M, K, N, plan_sm_count());
+  const GgPlan p = gg_plan(M, K, N, 0.43, plan_sm_count());
   return gg_layout(p, M, N, lddy, bi_b_bytes(p, N, K, nm_m)).total;
 }
 
@@ -614,7 +614,7 @@ bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint
     if (st == BITLINEAR_OK) t_last_kernel = "backward_input_few";
     return st;
   }
-  const GgPlan p = gg_plan(M, K, N, dev->sm_count);
+  const GgPlan p = gg_plan(M, K, N, 0.43, dev->sm_count);
   const GgLayout l = gg_layout(p, M, N, lddy, bi_b_bytes(p, N, K, w->nm_m));
   if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);

@@ -67,17 +67,20 @@ struct GradArgs {
   int32_t* status;
 };
 
+constexpr int kGgOutRow = 36;  // floats of a row of it: eight rows apart by 4 banks
+
 template <bool kWeight, bool kDense>
 struct GG {
   static constexpr int A_STAGE = 128 * kGgRed * 2;  // 16 KB
   static constexpr int OP = 128 * kGgRed * 2;       // 16 KB of B: [2 blocks of 64 columns][64 lines][128 B]
   // what lands of B: the operand itself, or compressed rows of 128 codes, 1 or 1/4 byte each
   static constexpr int RAW = kDense ? OP : kWeight ? kGgRed * 128 : kGgRed * 32;
-  static constexpr int S = kDense ? 6 : kWeight ? 6 : 8;
+  static constexpr int S = 6;
   static constexpr int R = kDense ? S : 4;          // S >= R: an operand slot's wait is on the stage that filled it
   static constexpr int GROUPS = kDense ? 0 : kGgGroups;
   static constexpr int THREADS = 32 * (8 + 4 * GROUPS);
-  static constexpr int FIXED = 512;
+  static constexpr int OUT = 4 * 32 * kGgOutRow * 4;  // a 32 x 32 tile of results for each storing warp
+  static constexpr int FIXED = OUT + 512;
   static constexpr int SMEM = S * (A_STAGE + RAW) + (kDense ? 0 : R * OP) + FIXED;
   static constexpr uint32_t IDESC = idesc_bf16(kGgRows, kGgCols, kWeight, true);
   static_assert(SMEM <= kTcSmemMax, "shared memory");
@@ -173,6 +176,29 @@ __device__ __forceinline__ void grad_store(const GradArgs& a, int64_t row, int c
   }
 }
 
+// A warp's 32 x 32 tile (rows from row0, columns from col) that lies in shared memory, for rows that 32-byte stores
+// cannot take: a row a step, lanes side by side (1000 x 2561 x 2559, dW: 42 us; element by element from each lane's own
+// row 83).  Where they can, a row a lane is faster (2048 x 6912 x 2560, dx: 57 us against 60 through shared memory).
+template <bool kWeight>
+__device__ __forceinline__ void grad_store_tile(const GradArgs& a, int64_t row0, int col, const float* tile,
+                                                float alpha) {
+  const int lane = threadIdx.x & 31;
+  if (col + lane >= a.cols) return;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    if (row0 + r >= a.rows) break;
+    const int64_t at = (row0 + r) * a.cols + col + lane;
+    float v = tile[r * kGgOutRow + lane];
+    if (kWeight) {
+      a.dw[at] = a.accumulate ? __fadd_rn(a.dw[at], v) : v;
+    } else {
+      v = __fmul_rn(v, alpha);
+      if (a.add) v = __fadd_rn(v, bf16_bits_to_f32(a.add[at]));
+      a.dx[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f));
+    }
+  }
+}
+
 // mapA: dy; box 128 bytes x 128 rows (dx) or 128 bytes x 64 rows (dW), landed 128-byte-swizzled.
 // mapB: the compressed rows; box 32 bytes (2-bit) or 128 bytes (8-bit) x 64 rows, landed as they are; with kDense the
 // bf16 rows, box 128 bytes x 64 rows, landed 128-byte-swizzled.
@@ -191,7 +217,8 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
   uint8_t* sA = smem_raw;                   // [S][16 KB]
   uint8_t* sOp = sA + S * C::A_STAGE;       // [R][OP]
   uint8_t* sRaw = sOp + (kDense ? 0 : R * C::OP);  // [S][RAW]; kDense: the operand slots themselves
-  uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + S * C::RAW);
+  float* sOut = reinterpret_cast<float*>(sRaw + S * C::RAW);  // [4][32][kGgOutRow]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + S * C::RAW + C::OUT);
   uint64_t* empty = full + S;
   uint64_t* opready = empty + S;     // [R] rank 0's: both CTAs' expanding warps (kDense: their forwarding threads)
   uint64_t* accfull = opready + R;   // [2]
@@ -421,11 +448,12 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       const int buf = t & 1;
       int row0, col0, kb0;
       unit_of(g, row0, col0, kb0);
-      const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
+      const int wrow = static_cast<int>(rank) * 128 + q * 32;  // the warp's first row of the tile
       const bool part = g >= a.full && a.split > 1;
+      float* out = sOut + q * 32 * kGgOutRow;
       constexpr int kAdd = kWeight ? 32 : 16;
-      uint32_t s0[kAdd];
-      if (!part) grad_addend<kWeight, 32>(a, row0 + lrow, col0, s0);
+      uint32_t s0[kAdd], s1[kAdd];
+      if (!part) grad_addend<kWeight, 32>(a, row0 + wrow + lane, col0, s0);
       if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
         *a.status = kDevTimeoutEpilogue;
         break;
@@ -433,20 +461,27 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < kGgCols; c0 += 32) {
-        uint32_t w[32], s1[kAdd];
+        uint32_t w[32];
         tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
-        if (!part && c0 + 32 < kGgCols) grad_addend<kWeight, 32>(a, row0 + lrow, col0 + c0 + 32, s1);
+        if (!part && c0 + 32 < kGgCols) grad_addend<kWeight, 32>(a, row0 + wrow + lane, col0 + c0 + 32, s1);
         tc_wait_ld();
         float v[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
           v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
         if (part) {
-          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + lrow) * 8;
+          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + wrow + lane) * 8;
 #pragma unroll
           for (int c = 0; c < 4; ++c) st_global_v8(p + c * 8 * kGgRows, reinterpret_cast<const uint32_t*>(v + 8 * c));
-        } else if (row0 + lrow < a.rows && col0 + c0 < a.cols) {
-          grad_store<kWeight, 32>(a, row0 + lrow, col0 + c0, v, s0, alpha);
+        } else if (a.vec && col0 + c0 + 32 <= a.cols) {
+          if (row0 + wrow + lane < a.rows) grad_store<kWeight, 32>(a, row0 + wrow + lane, col0 + c0, v, s0, alpha);
+        } else if (row0 + wrow < a.rows && col0 + c0 < a.cols) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<float4*>(out + lane * kGgOutRow + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+          __syncwarp();
+          grad_store_tile<kWeight>(a, row0 + wrow, col0 + c0, out, alpha);
+          __syncwarp();
         }
 #pragma unroll
         for (int i = 0; i < kAdd; ++i) s0[i] = s1[i];
