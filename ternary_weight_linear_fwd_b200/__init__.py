@@ -8,9 +8,12 @@ built, or the device is not sm_100, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
+
+import torch
 
 __all__ = [
     "BitLinearError", "PackedWeights", "lib", "packed_layout", "pack_weights", "pack_ternary",
@@ -425,13 +428,13 @@ class _Here:
 
 
 _HERE_CTX = _Here()
+_BF16, _F32, _I8, _I32 = torch.bfloat16, torch.float32, torch.int8, torch.int32
 
 
 def _on(device, stream):
     """Context in which a call's outputs and workspace are allocated and its kernels are launched."""
-    import torch
     if stream is None:
-        if device.type == "cuda" and device.index == torch.cuda.current_device():
+        if device.index is not None and device.index == torch._C._cuda_getDevice():
             return _HERE_CTX  # entering torch.cuda.device costs more than a small kernel
         return torch.cuda.device(device)
     if stream.device != device:
@@ -441,21 +444,19 @@ def _on(device, stream):
 
 def _raw_stream(device, stream) -> int:
     """The address of `stream`, or of the device's current stream (without building a Stream object for it)."""
-    import torch
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _mat(t, what: str, dtype, device=None, shape=None, align: int = 1):
     """A 2-D CUDA matrix as the kernels read it: (the tensor, its row stride).  Views with unit stride inside a
     row and rows that do not overlap pass as they are; others (expanded, transposed, misaligned) are copied."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == 2):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.is_cuda):
         raise ValueError(f"{what}: expected a 2-D {dtype} CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{what}: expected a tensor on {device}, got one on {t.device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous() and t.data_ptr() % align == 0:
+    if t.is_contiguous() and (align == 1 or t.data_ptr() % align == 0):
         return t, t.shape[1]
     M, K = t.shape
     ok = (K == 1 or t.stride(1) == 1) and (M == 1 or t.stride(0) >= K) and t.data_ptr() % align == 0
@@ -466,40 +467,42 @@ def _mat(t, what: str, dtype, device=None, shape=None, align: int = 1):
 
 def _new(like, dtype=None):
     """An uninitialised contiguous tensor of the same shape and device."""
-    import torch
     return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
 
-def _vec(t, what: str, n: int, device, dtype=None):
-    import torch
-    dtype = dtype or torch.float32
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == 1 and t.shape[0] == n
+def _vec(t, what: str, n: int, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.dim() == 1 and t.shape[0] == n
             and t.device == device):
-        raise ValueError(f"{what}: expected a {dtype} tensor of {n} elements on {device}")
-    return t.contiguous()
+        raise ValueError(f"{what}: expected a {_F32} tensor of {n} elements on {device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(device: int, query: str, *sizes) -> int:
+    """The C library's answer for a call of these sizes on this (the current) device."""
+    return int(getattr(lib(), query)(*sizes))
 
 
 def _scratch(workspace, need: int, device):
     """The caller's workspace, checked, or one of the size the call needs: (tensor or None, bytes)."""
-    import torch
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
     _check_workspace(workspace, device)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def layernorm(x, weight, bias=None, eps: float = 1e-5, want_stats: bool = False, out=None, stream=None):
     """Layer norm of each row of a bf16 [M, K] matrix (weight, bias fp32 [K]): y bf16 [M, K]; with want_stats
     (y, mean, rstd), the fp32 [M] moments that layernorm_backward takes."""
-    import torch
     with _on(x.device, stream):
-        x, ldx = _mat(x, "x", torch.bfloat16)
+        x, ldx = _mat(x, "x", _BF16)
         M, K = x.shape
         weight = _vec(weight, "weight", K, x.device)
         bias = None if bias is None else _vec(bias, "bias", K, x.device)
-        _check_out(out, (M, K), torch.bfloat16, x.device, "out")
+        if out is not None:
+            _check_out(out, (M, K), _BF16, x.device, "out")
         y = out if out is not None else _new(x)
-        mean = torch.empty(M, dtype=torch.float32, device=x.device) if want_stats else None
+        mean = torch.empty(M, dtype=_F32, device=x.device) if want_stats else None
         rstd = _new(mean) if want_stats else None
         _check(lib().bitlinear_layernorm(_ptr(x), ldx, M, K, _ptr(weight), _ptr(bias), float(eps), _ptr(y),
                                          _ptr(mean), _ptr(rstd), _raw_stream(x.device, stream)), "layernorm")
@@ -510,15 +513,14 @@ def layernorm_quant_act(x, weight, bias=None, eps: float = 1e-5, rowsum: bool = 
                         stream=None):
     """Layer norm, then the per-token int8 codes of the result: (q, gamma, rowsum or None), with want_stats
     also mean and rstd.  The codes feed forward_q8 and, kept, backward_weight."""
-    import torch
     with _on(x.device, stream):
-        x, ldx = _mat(x, "x", torch.bfloat16)
+        x, ldx = _mat(x, "x", _BF16)
         M, K = x.shape
         weight = _vec(weight, "weight", K, x.device)
         bias = None if bias is None else _vec(bias, "bias", K, x.device)
-        q = _new(x, torch.int8)
-        g = torch.empty(M, dtype=torch.float32, device=x.device)
-        rs = _new(g, torch.int32) if rowsum else None
+        q = _new(x, _I8)
+        g = torch.empty(M, dtype=_F32, device=x.device)
+        rs = _new(g, _I32) if rowsum else None
         mean = _new(g) if want_stats else None
         rstd = _new(g) if want_stats else None
         _check(lib().bitlinear_layernorm_quant_act(_ptr(x), ldx, M, K, _ptr(weight), _ptr(bias), float(eps), _ptr(q),
@@ -534,16 +536,16 @@ def norm_backward_workspace_bytes(M: int, K: int) -> int:
 def layernorm_backward(dy, x, weight, mean, rstd, want_bias: bool = True, workspace=None, stream=None):
     """Gradients of layernorm: (dx bf16 [M, K], dweight fp32 [K], dbias fp32 [K] or None) from the output's
     gradient dy and the forward call's x, mean and rstd."""
-    import torch
     with _on(x.device, stream):
-        x, ldx = _mat(x, "x", torch.bfloat16)
+        x, ldx = _mat(x, "x", _BF16)
         M, K = x.shape
-        dy, lddy = _mat(dy, "dy", torch.bfloat16, x.device, (M, K))
+        dy, lddy = _mat(dy, "dy", _BF16, x.device, (M, K))
         weight = _vec(weight, "weight", K, x.device)
         mean, rstd = _vec(mean, "mean", M, x.device), _vec(rstd, "rstd", M, x.device)
         dx, dw = _new(x), _new(weight)
         db = _new(weight) if want_bias else None
-        workspace, n = _scratch(workspace, norm_backward_workspace_bytes(M, K), x.device)
+        workspace, n = _scratch(
+            workspace, _workspace_bytes(x.device.index, "bitlinear_norm_backward_workspace_bytes", M, K), x.device)
         _check(lib().bitlinear_layernorm_backward(_ptr(dy), lddy, _ptr(x), ldx, M, K, _ptr(weight), _ptr(mean),
                                                   _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), n,
                                                   _raw_stream(x.device, stream)), "layernorm_backward")
@@ -552,14 +554,14 @@ def layernorm_backward(dy, x, weight, mean, rstd, want_bias: bool = True, worksp
 
 def rmsnorm_backward(dy, x, g, eps: float, workspace=None, stream=None):
     """Gradients of the RMSNorm of rmsnorm_quant_act / forward_norm: (dx bf16 [M, K], dg fp32 [K])."""
-    import torch
     with _on(x.device, stream):
-        x, ldx = _mat(x, "x", torch.bfloat16)
+        x, ldx = _mat(x, "x", _BF16)
         M, K = x.shape
-        dy, lddy = _mat(dy, "dy", torch.bfloat16, x.device, (M, K))
+        dy, lddy = _mat(dy, "dy", _BF16, x.device, (M, K))
         g = _vec(g, "g", K, x.device)
         dx, dg = _new(x), _new(g)
-        workspace, n = _scratch(workspace, norm_backward_workspace_bytes(M, K), x.device)
+        workspace, n = _scratch(
+            workspace, _workspace_bytes(x.device.index, "bitlinear_norm_backward_workspace_bytes", M, K), x.device)
         _check(lib().bitlinear_rmsnorm_backward(_ptr(dy), lddy, _ptr(x), ldx, M, K, _ptr(g), float(eps), _ptr(dx),
                                                 _ptr(dg), _ptr(workspace), n, _raw_stream(x.device, stream)), "rmsnorm_backward")
     return dx, dg
@@ -567,13 +569,13 @@ def rmsnorm_backward(dy, x, g, eps: float, workspace=None, stream=None):
 
 def dequant_act(q, gamma, out=None, stream=None):
     """The activation that per-token int8 codes stand for (bf16 [M, K]): bf16 of q * gamma / 127."""
-    import torch
     with _on(q.device, stream):
-        q, ldq = _mat(q, "q", torch.int8)
+        q, ldq = _mat(q, "q", _I8)
         M, K = q.shape
         gamma = _vec(gamma, "gamma", M, q.device)
-        _check_out(out, (M, K), torch.bfloat16, q.device, "out")
-        y = out if out is not None else _new(q, torch.bfloat16)
+        if out is not None:
+            _check_out(out, (M, K), _BF16, q.device, "out")
+        y = out if out is not None else _new(q, _BF16)
         _check(lib().bitlinear_dequant_act(_ptr(q), ldq, _ptr(gamma), M, K, _ptr(y), _raw_stream(q.device, stream)), "dequant_act")
     return y
 
@@ -593,14 +595,14 @@ class Relu2GluCheckpoint(NamedTuple):
 def relu2_glu_quant_act(g, u, stream=None) -> Relu2GluCheckpoint:
     """The gated FFN's h in a training step, as codes for the down projection's forward_q8, with the 8-bit
     checkpoints of g and u (bf16 [M, N], e.g. from forward_group) that relu2_glu_backward reads."""
-    import torch
     with _on(g.device, stream):
-        g, ldg = _mat(g, "g", torch.bfloat16)
+        g, ldg = _mat(g, "g", _BF16)
         M, N = g.shape
-        u, ldu = _mat(u, "u", torch.bfloat16, g.device, (M, N))
-        q0 = _new(g, torch.int8)
-        m0 = torch.empty(M, dtype=torch.float32, device=g.device)
-        q, m, rs = (q0, _new(q0), _new(q0)), (m0, _new(m0), _new(m0)), _new(m0, torch.int32)
+        u, ldu = _mat(u, "u", _BF16, g.device, (M, N))
+        q0 = _new(g, _I8)
+        q = q0, _new(q0), _new(q0)
+        *m, rs = torch.empty((4, M), dtype=_F32, device=g.device).unbind()
+        rs = rs.view(_I32)
         _check(lib().bitlinear_relu2_glu_quant_act(_ptr(g), ldg, _ptr(u), ldu, M, N, _ptr(q[0]), _ptr(m[0]),
                                                    _ptr(q[1]), _ptr(m[1]), _ptr(q[2]), _ptr(m[2]), _ptr(rs),
                                                    _raw_stream(g.device, stream)), "relu2_glu_quant_act")
@@ -609,12 +611,11 @@ def relu2_glu_quant_act(g, u, stream=None) -> Relu2GluCheckpoint:
 
 def relu2_glu_backward(dh, q_g, gamma_g, q_u, gamma_u, stream=None):
     """Gradients of the gate's and up projection's outputs, (dg, du) bf16 [M, N], from dh and the checkpoints."""
-    import torch
     with _on(dh.device, stream):
-        dh, lddh = _mat(dh, "dh", torch.bfloat16)
+        dh, lddh = _mat(dh, "dh", _BF16)
         M, N = dh.shape
-        _check_out(q_g, (M, N), torch.int8, dh.device, "q_g")
-        _check_out(q_u, (M, N), torch.int8, dh.device, "q_u")
+        _check_out(q_g, (M, N), _I8, dh.device, "q_g")
+        _check_out(q_u, (M, N), _I8, dh.device, "q_u")
         gamma_g, gamma_u = _vec(gamma_g, "gamma_g", M, dh.device), _vec(gamma_u, "gamma_u", M, dh.device)
         dg, du = _new(dh), _new(dh)
         _check(lib().bitlinear_relu2_glu_backward(_ptr(dh), lddh, _ptr(q_g), _ptr(gamma_g), _ptr(q_u), _ptr(gamma_u),
@@ -632,20 +633,22 @@ def backward_weight(dy, q, gamma, out=None, accumulate: bool = False, workspace=
     """Gradient of a BitLinear's latent weights: dW = dy^T x~ (fp32 [N, K]) from the output's gradient dy (bf16
     [M, N]) and the 8-bit checkpoint (q, gamma) of its input, as quant_act, rmsnorm_quant_act,
     layernorm_quant_act or relu2_glu_quant_act wrote it.  accumulate: add to `out`, which is then needed."""
-    import torch
     with _on(dy.device, stream):
-        dy, lddy = _mat(dy, "dy", torch.bfloat16, align=16)
+        dy, lddy = _mat(dy, "dy", _BF16, align=16)
         M, N = dy.shape
-        q, ldq = _mat(q, "q", torch.int8, dy.device, align=16)
+        q, ldq = _mat(q, "q", _I8, dy.device, align=16)
         K = q.shape[1]
         if q.shape[0] != M:
             raise ValueError(f"backward_weight: dy has {M} rows, q has {q.shape[0]}")
         gamma = _vec(gamma, "gamma", M, dy.device)
-        _check_out(out, (N, K), torch.float32, dy.device, "out")
+        if out is not None:
+            _check_out(out, (N, K), _F32, dy.device, "out")
         if accumulate and out is None:
             raise ValueError("backward_weight: accumulate needs out")
-        dW = out if out is not None else torch.empty((N, K), dtype=torch.float32, device=dy.device)
-        workspace, n = _scratch(workspace, backward_weight_workspace_bytes(M, N, K, lddy, ldq), dy.device)
+        dW = out if out is not None else dy.new_empty((N, K), dtype=_F32)
+        workspace, n = _scratch(
+            workspace, _workspace_bytes(dy.device.index, "bitlinear_backward_weight_workspace_bytes", M, N, K, lddy, ldq),
+            dy.device)
         _check(lib().bitlinear_backward_weight(_ptr(dy), lddy, _ptr(q), ldq, _ptr(gamma), M, N, K, _ptr(dW),
                                                _ptr(workspace), n, FLAG_ACCUMULATE if accumulate else 0,
                                                _raw_stream(dy.device, stream)), "backward_weight")
@@ -660,18 +663,21 @@ def backward_input_workspace_bytes(w: PackedWeights, M: int, lddy: Optional[int]
 def backward_input(w: PackedWeights, dy, add=None, out=None, workspace=None, stream=None):
     """Gradient of a BitLinear's input: dx = alpha dy W_t (+ add), bf16 [M, K], dense or N:M weights; add is the
     gradient that reaches the same input another way (bf16 [M, K])."""
-    import torch
     with _on(dy.device, stream):
-        dy, lddy = _mat(dy, "dy", torch.bfloat16, align=16)
+        dy, lddy = _mat(dy, "dy", _BF16, align=16)
         M = dy.shape[0]
         if dy.shape[1] != w.N:
             raise ValueError(f"backward_input: dy has {dy.shape[1]} columns, the weights have {w.N} rows")
         if w.codes.device != dy.device:
             raise ValueError(f"backward_input: weights on {w.codes.device}, dy on {dy.device}")
-        _check_out(add, (M, w.K), torch.bfloat16, dy.device, "add")
-        _check_out(out, (M, w.K), torch.bfloat16, dy.device, "out")
-        dx = out if out is not None else torch.empty((M, w.K), dtype=torch.bfloat16, device=dy.device)
-        workspace, n = _scratch(workspace, backward_input_workspace_bytes(w, M, lddy), dy.device)
+        if add is not None:
+            _check_out(add, (M, w.K), _BF16, dy.device, "add")
+        if out is not None:
+            _check_out(out, (M, w.K), _BF16, dy.device, "out")
+        dx = out if out is not None else dy.new_empty((M, w.K))
+        workspace, n = _scratch(
+            workspace, _workspace_bytes(dy.device.index, "bitlinear_backward_input_workspace_bytes", M, w.N, w.K, lddy,
+                                        w.nm_n, w.nm_m), dy.device)
         ws = w.c_struct()
         _check(lib().bitlinear_backward_input(ctypes.byref(ws), _ptr(dy), lddy, M, _ptr(add), _ptr(dx),
                                               _ptr(workspace), n, _raw_stream(dy.device, stream)), "backward_input")
