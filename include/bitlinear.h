@@ -499,7 +499,8 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
  * workspace, workspace_bytes: device scratch of at least
  *          bitlinear_backward_weight_workspace_bytes(M, N, K, lddy, ldq), 32-byte
  *          aligned (may be NULL when that is 0).
- * flags    BITLINEAR_FLAG_ACCUMULATE.
+ * flags    BITLINEAR_FLAG_ACCUMULATE.  A sum below 2^-126 in magnitude may then
+ *          become 0 (the additions are made in memory).
  * Errors: NULL, SHAPE, ALIGN, WORKSPACE, FLAGS, DEVICE, CUDA. */
 size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq);
 bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, const int8_t* q, int64_t ldq,

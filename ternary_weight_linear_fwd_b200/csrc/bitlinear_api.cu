@@ -124,12 +124,13 @@ struct MapCache {
 };
 thread_local MapCache t_maps;
 
-// 2-D uint8 tensor map: inner extent `inner` bytes, `outer` rows of `stride`
-// bytes, box {box_inner, box_outer}; out-of-range elements read as zero.
-// swizzle: 0 (none), 32, 64 or 128 (the shared-memory swizzle of the landed box, in bytes).
-bool make_map_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t stride,
-                 uint32_t box_inner, uint32_t box_outer, int swizzle) {
-  const MapKey k{base, inner, outer, stride, box_inner, box_outer, static_cast<uint32_t>(swizzle)};
+// 2-D tensor map: inner extent `inner` elements, `outer` rows of `stride` bytes,
+// box {box_inner, box_outer}; out-of-range elements read as zero.
+// swizzle: 0 (none), 32, 64 or 128 (the shared-memory swizzle of the box, in bytes).
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
+              uint64_t stride, uint32_t box_inner, uint32_t box_outer, int swizzle) {
+  const MapKey k{base, inner, outer, stride, box_inner, box_outer,
+                 static_cast<uint32_t>(swizzle) | static_cast<uint32_t>(type) << 16};
   MapCache& c = t_maps;
   for (int i = 0; i < kMapCache; ++i)
     if (c.used[i] && c.key[i] == k) {
@@ -142,7 +143,7 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
   const cuuint64_t strides[1] = {stride};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                   : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
@@ -155,6 +156,10 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
   c.used[c.next] = true;
   c.next = (c.next + 1) % kMapCache;
   return true;
+}
+bool make_map_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t stride,
+                 uint32_t box_inner, uint32_t box_outer, int swizzle) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, stride, box_inner, box_outer, swizzle);
 }
 
 // Largest dynamic shared memory already granted to a kernel on a device

@@ -262,10 +262,10 @@ bitlinear_status gg_dy(const uint16_t** dy, int64_t lddy, int M, int N, uint8_t*
 }
 
 template <bool kWeight>
-bitlinear_status gg_launch(const CUtensorMap& mA, const CUtensorMap& mB, const GradArgs& a, const GgPlan& p,
-                           bool dense, cudaStream_t s) {
+bitlinear_status gg_launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC, const GradArgs& a,
+                           const GgPlan& p, bool dense, cudaStream_t s) {
   auto go = [&](auto kern, int threads, size_t smem) {
-    return launch_ex(kern, dim3(2 * p.pairs), dim3(threads), smem, s, true, 2, mA, mB, a);
+    return launch_ex(kern, dim3(2 * p.pairs), dim3(threads), smem, s, true, 2, mA, mB, mC, a);
   };
   bitlinear_status st = dense ? go(grad_gemm_kernel<kWeight, true>, GG<kWeight, true>::THREADS, GG<kWeight, true>::SMEM)
                               : go(grad_gemm_kernel<kWeight, false>, GG<kWeight, false>::THREADS,
@@ -562,7 +562,15 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   a.dw = dW;
   a.accumulate = (flags & BITLINEAR_FLAG_ACCUMULATE) != 0;
   a.vec = K % 8 == 0 && aligned32(dW);
-  st = gg_launch<true>(mA, mB, a, p, dense, s);
+  // Stores by TMA go through shared memory, which the MMAs of the next tile need: 16 x 2560 x 6912 took 19.5 us with a
+  // row a lane (32 lines an instruction) and 15.4 by TMA, but 4096 x 11008 x 2048 132 and 140.  So TMA where no next
+  // tile's k-blocks run beside the stores or only a few do, where it saves the reads of an accumulation, and for rows
+  // that 32-byte stores cannot take.
+  a.tma = K % 4 == 0 && aligned16(dW) && (a.accumulate || !a.vec || p.units <= p.pairs || p.kblocks <= 8);
+  CUtensorMap mC = mA;
+  if (a.tma && !make_map(&mC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dW, K, N, 4 * static_cast<uint64_t>(K), 32, 32, 128))
+    return BITLINEAR_ERR_CUDA;
+  st = gg_launch<true>(mA, mB, mC, a, p, dense, s);
   if (st == BITLINEAR_OK) t_last_kernel = "backward_weight";
   return st;
 }
@@ -638,7 +646,7 @@ bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint
   a.add = add;
   a.dx = dx;
   a.vec = K % 16 == 0 && aligned32(dx) && aligned32(add);
-  st = gg_launch<false>(mA, mB, a, p, dense, s);
+  st = gg_launch<false>(mA, mB, mA, a, p, dense, s);
   if (st == BITLINEAR_OK) t_last_kernel = "backward_input";
   return st;
 }

@@ -31,7 +31,7 @@
 // halve.  Rings as in gemm_tc2.cuh: S copy stages of 64 steps of the reduction
 // (A's tile by TMA, the compressed rows), R operand slots (expanded B).  Roles:
 // warp 0 copies, warp 1 (rank 0) issues the MMAs, warp 2 owns TMEM, warps 4 ..
-// 11 expand (two groups, alternate stages), warps 12 .. 15 store.
+// 11 expand (two groups, alternate stages), the last eight store.
 //
 // Persistent: one pair per two SMs walks a static list of units.  The tiles
 // that fill whole rounds of pairs run over their whole reduction; the rest are
@@ -46,6 +46,7 @@ namespace bl {
 constexpr int kGgRows = 256;      // rows of a pair tile (128 a CTA)
 constexpr int kGgCols = 256;      // columns of a pair tile (128 of B a CTA)
 constexpr int kGgRed = 64;        // steps of the reduction per stage
+constexpr int kGgStoring = 8;      // storing warps, two for each 32 rows: one waits for memory while the other computes
 constexpr int kGgGroups = 2;       // groups of four expanding warps, taking the stages in turn
 constexpr int kGgSlab = kGgRows * kGgCols;  // fp32 of one part of a split tile
 
@@ -63,11 +64,10 @@ struct GradArgs {
   float* dw;              // dW: fp32 [rows, cols]
   int accumulate;         // dW: add to it
   int vec;                // output (and add) rows are 32-byte aligned
+  int tma;                // dW: stored (or added) by TMA
   float* slab;            // [(tiles - full) * split][32 groups of 8 columns][256 rows][8]: a warp's store is contiguous
   int32_t* status;
 };
-
-constexpr int kGgOutRow = 36;  // floats of a row of it: eight rows apart by 4 banks
 
 template <bool kWeight, bool kDense>
 struct GG {
@@ -75,11 +75,11 @@ struct GG {
   static constexpr int OP = 128 * kGgRed * 2;       // 16 KB of B: [2 blocks of 64 columns][64 lines][128 B]
   // what lands of B: the operand itself, or compressed rows of 128 codes, 1 or 1/4 byte each
   static constexpr int RAW = kDense ? OP : kWeight ? kGgRed * 128 : kGgRed * 32;
-  static constexpr int S = 6;
+  static constexpr int S = kWeight && !kDense ? 5 : 6;
   static constexpr int R = kDense ? S : 4;          // S >= R: an operand slot's wait is on the stage that filled it
   static constexpr int GROUPS = kDense ? 0 : kGgGroups;
-  static constexpr int THREADS = 32 * (8 + 4 * GROUPS);
-  static constexpr int OUT = 4 * 32 * kGgOutRow * 4;  // a 32 x 32 tile of results for each storing warp
+  static constexpr int THREADS = 32 * (4 + 4 * GROUPS + kGgStoring);
+  static constexpr int OUT = kGgStoring * 4096;     // a 32 x 32 tile of results for each storing warp
   static constexpr int FIXED = OUT + 512;
   static constexpr int SMEM = S * (A_STAGE + RAW) + (kDense ? 0 : R * OP) + FIXED;
   static constexpr uint32_t IDESC = idesc_bf16(kGgRows, kGgCols, kWeight, true);
@@ -176,9 +176,20 @@ __device__ __forceinline__ void grad_store(const GradArgs& a, int64_t row, int c
   }
 }
 
-// A warp's 32 x 32 tile (rows from row0, columns from col) that lies in shared memory, for rows that 32-byte stores
-// cannot take: a row a step, lanes side by side (1000 x 2561 x 2559, dW: 42 us; element by element from each lane's own
-// row 83).  Where they can, a row a lane is faster (2048 x 6912 x 2560, dx: 57 us against 60 through shared memory).
+// A warp's 32 x 32 tile of results in shared memory, rows of 128 bytes with the 128-byte swizzle (which TMA undoes).
+__device__ __forceinline__ void grad_tile_put(float* tile, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(tile + lane * 32 + 4 * (c ^ (lane & 7))) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+__device__ __forceinline__ float grad_tile_get(const float* tile, int r, int c) {
+  return tile[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)];
+}
+
+// Such a tile (rows from row0, columns from col) to rows that neither TMA nor 32-byte stores can take: a row a step,
+// lanes side by side (1000 x 2561 x 2559, dW: 42 us; element by element from each lane's own row 83).
 template <bool kWeight>
 __device__ __forceinline__ void grad_store_tile(const GradArgs& a, int64_t row0, int col, const float* tile,
                                                 float alpha) {
@@ -188,7 +199,7 @@ __device__ __forceinline__ void grad_store_tile(const GradArgs& a, int64_t row0,
   for (int r = 0; r < 32; ++r) {
     if (row0 + r >= a.rows) break;
     const int64_t at = (row0 + r) * a.cols + col + lane;
-    float v = tile[r * kGgOutRow + lane];
+    float v = grad_tile_get(tile, r, lane);
     if (kWeight) {
       a.dw[at] = a.accumulate ? __fadd_rn(a.dw[at], v) : v;
     } else {
@@ -201,11 +212,11 @@ __device__ __forceinline__ void grad_store_tile(const GradArgs& a, int64_t row0,
 
 // mapA: dy; box 128 bytes x 128 rows (dx) or 128 bytes x 64 rows (dW), landed 128-byte-swizzled.
 // mapB: the compressed rows; box 32 bytes (2-bit) or 128 bytes (8-bit) x 64 rows, landed as they are; with kDense the
-// bf16 rows, box 128 bytes x 64 rows, landed 128-byte-swizzled.
+// bf16 rows, box 128 bytes x 64 rows, landed 128-byte-swizzled.  mapC (dW, a.tma): fp32, box 32 x 32, 128-byte-swizzled.
 template <bool kWeight, bool kDense>
 __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     grad_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                     const GradArgs a) {
+                     const __grid_constant__ CUtensorMap mapC, const GradArgs a) {
   using C = GG<kWeight, kDense>;
   constexpr int S = C::S, R = C::R, G = C::GROUPS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
   uint8_t* sA = smem_raw;                   // [S][16 KB]
   uint8_t* sOp = sA + S * C::A_STAGE;       // [R][OP]
   uint8_t* sRaw = sOp + (kDense ? 0 : R * C::OP);  // [S][RAW]; kDense: the operand slots themselves
-  float* sOut = reinterpret_cast<float*>(sRaw + S * C::RAW);  // [4][32][kGgOutRow]
+  float* sOut = reinterpret_cast<float*>(sRaw + S * C::RAW);  // [kGgStoring][32][32]
   uint64_t* full = reinterpret_cast<uint64_t*>(sRaw + S * C::RAW + C::OUT);
   uint64_t* empty = full + S;
   uint64_t* opready = empty + S;     // [R] rank 0's: both CTAs' expanding warps (kDense: their forwarding threads)
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     for (int j = 0; j < R; ++j) mbar_init(&opready[j], kDense ? 2 : 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
-      mbar_init(&accempty[b], 8);
+      mbar_init(&accempty[b], 2 * kGgStoring);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -440,9 +451,13 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     }
   } else if (warp >= 4 + 4 * G) {
     // -------------------------------------------------------------- stores (both CTAs, own rows)
-    const int q = warp - 4 - 4 * G;
+    const int q = warp & 3, first = ((warp - 4 - 4 * G) >> 2) * 32;  // 32 rows, every other 32 columns
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float alpha = kWeight ? 1.0f : *a.alpha;
+    // dW's plain stores beside the next tile's k-blocks are left to the first four warps (2048 x 2560 x 6912: 61.4 us
+    // against 65 with all eight)
+    const bool solo = kWeight && !a.tma;
+    const int step = solo ? 32 : 64;
     int t = 0;
     for (int g = pair; g < a.units; g += npairs, ++t) {
       const int buf = t & 1;
@@ -450,46 +465,68 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       unit_of(g, row0, col0, kb0);
       const int wrow = static_cast<int>(rank) * 128 + q * 32;  // the warp's first row of the tile
       const bool part = g >= a.full && a.split > 1;
-      float* out = sOut + q * 32 * kGgOutRow;
-      constexpr int kAdd = kWeight ? 32 : 16;
-      uint32_t s0[kAdd], s1[kAdd];
-      if (!part) grad_addend<kWeight, 32>(a, row0 + wrow + lane, col0, s0);
+      float* out = sOut + (warp - 4 - 4 * G) * 1024;
+      uint32_t s0[16], s1[16];
+      if (!kWeight && !part) grad_addend<false, 32>(a, row0 + wrow + lane, col0 + first, s0);
       if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
         *a.status = kDevTimeoutEpilogue;
         break;
       }
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < kGgCols; c0 += 32) {
+      for (int c0 = solo && first ? kGgCols : first; c0 < kGgCols; c0 += step) {
         uint32_t w[32];
         tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
-        if (!part && c0 + 32 < kGgCols) grad_addend<kWeight, 32>(a, row0 + wrow + lane, col0 + c0 + 32, s1);
+        if (!kWeight && !part && c0 + step < kGgCols)
+          grad_addend<false, 32>(a, row0 + wrow + lane, col0 + c0 + step, s1);
         tc_wait_ld();
         float v[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
           v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
-        if (part) {
-          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + wrow + lane) * 8;
+        if (row0 + wrow < a.rows && col0 + c0 < a.cols) {
+          if (part) {
+            float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + wrow + lane) * 8;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) st_global_v8(p + c * 8 * kGgRows, reinterpret_cast<const uint32_t*>(v + 8 * c));
-        } else if (a.vec && col0 + c0 + 32 <= a.cols) {
-          if (row0 + wrow + lane < a.rows) grad_store<kWeight, 32>(a, row0 + wrow + lane, col0 + c0, v, s0, alpha);
-        } else if (row0 + wrow < a.rows && col0 + c0 < a.cols) {
+            for (int c = 0; c < 4; ++c) st_global_v8(p + c * 8 * kGgRows, reinterpret_cast<const uint32_t*>(v + 8 * c));
+          } else if (!kWeight && a.vec && col0 + c0 + 32 <= a.cols) {
+            if (row0 + wrow + lane < a.rows)
+              grad_store<false, 32>(a, row0 + wrow + lane, col0 + c0, v, s0, alpha);
+          } else if (kWeight && a.tma) {
+            if (lane == 0) bulk_wait_read<0>();  // the last store has read the tile
+            __syncwarp();
+            grad_tile_put(out, v);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (a.accumulate)
+                tma_add_2d(&mapC, col0 + c0, row0 + wrow, out);
+              else
+                tma_store_2d(&mapC, col0 + c0, row0 + wrow, out);
+              bulk_commit();
+            }
+          } else if (kWeight && a.vec && !a.accumulate && col0 + c0 + 32 <= a.cols) {
+            if (row0 + wrow + lane < a.rows) {
+              float* p = a.dw + static_cast<int64_t>(row0 + wrow + lane) * a.cols + col0 + c0;
 #pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<float4*>(out + lane * kGgOutRow + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-          __syncwarp();
-          grad_store_tile<kWeight>(a, row0 + wrow, col0 + c0, out, alpha);
-          __syncwarp();
+              for (int c = 0; c < 32; c += 8) st_global_v8(p + c, reinterpret_cast<const uint32_t*>(v + c));
+            }
+          } else {
+            grad_tile_put(out, v);
+            __syncwarp();
+            grad_store_tile<kWeight>(a, row0 + wrow, col0 + c0, out, alpha);
+            __syncwarp();
+          }
         }
+        if (!kWeight)
 #pragma unroll
-        for (int i = 0; i < kAdd; ++i) s0[i] = s1[i];
+          for (int i = 0; i < 16; ++i) s0[i] = s1[i];
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote_cta(accempty0 + static_cast<uint32_t>(buf * 8));
     }
+    if (kWeight && lane == 0) bulk_wait<0>();  // results are in memory before the CTA ends
   }
   tc_fence_before();
   __syncthreads();
