@@ -410,23 +410,32 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
     for (int i = 0; i < 4; ++i) dwv[j][i] = dbv[j][i] = splat2(0.0f);
   uint32_t nx[G][4], ny[G][4];  // the next row's words
   float nmean = 0.0f, nrstd = 1.0f;
-  auto load = [&](int64_t row) {
+  int64_t row = static_cast<int64_t>(blockIdx.x) * a.rg + grp;
+  // the thread's first chunk of the row to load next and of the row to write, and the steps between a group's rows
+  const uint16_t* px = a.x + row * a.ldx + 8 * t;
+  const uint16_t* py = a.dy + row * a.lddy + 8 * t;
+  uint16_t* pd = a.dx + row * K + 8 * t;
+  const int64_t sx = stride * a.ldx, sy = stride * a.lddy, sd = stride * K;
+  auto load = [&](int64_t row) {  // advances px and py
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int c = t + j * T;
       if (kFast) {
-        const uint4 p = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + 8 * min(c, chunks - 1));
-        const uint4 q = *reinterpret_cast<const uint4*>(a.dy + row * a.lddy + 8 * min(c, chunks - 1));
+        const int at = 8 * j * T - (j == G - 1 && c >= chunks ? 8 * (c - chunks + 1) : 0);
+        const uint4 p = *reinterpret_cast<const uint4*>(px + at);
+        const uint4 q = *reinterpret_cast<const uint4*>(py + at);
         nx[j][0] = p.x; nx[j][1] = p.y; nx[j][2] = p.z; nx[j][3] = p.w;
         ny[j][0] = q.x; ny[j][1] = q.y; ny[j][2] = q.z; ny[j][3] = q.w;
       } else if (c < chunks) {
-        load8_raw(a.x + row * a.ldx, 8 * c, K, vx, nx[j]);
-        load8_raw(a.dy + row * a.lddy, 8 * c, K, vdy, ny[j]);
+        load8_raw(px - 8 * t, 8 * c, K, vx, nx[j]);
+        load8_raw(py - 8 * t, 8 * c, K, vdy, ny[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) nx[j][i] = ny[j][i] = 0u;
       }
     }
+    px += sx;
+    py += sy;
     if (kLayer) {
       nmean = a.mean[row];
       nrstd = a.rstd[row];
@@ -440,7 +449,6 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
     w[3] = make_float2(q.z, q.w);
   };
   __syncthreads();
-  int64_t row = static_cast<int64_t>(blockIdx.x) * a.rg + grp;
   if (kAhead && row < a.M) load(row);
   for (int it = 0; row < a.M; row += stride, it ^= 1) {
     if (!kAhead) load(row);
@@ -472,13 +480,15 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
       }
     }
     float c1 = p1.x + p1.y, c2 = p2.x + p2.y;
+    {  // both sums in one butterfly: the lower half-warp's lanes take the first, the upper's the second
+      float v = lane < 16 ? c1 : c2;
+      v += __shfl_xor_sync(0xffffffffu, lane < 16 ? c2 : c1, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      c1 += __shfl_xor_sync(0xffffffffu, c1, o);
-      c2 += __shfl_xor_sync(0xffffffffu, c2, o);
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      c1 = v;
     }
     if (nw > 1) {
-      if (lane == 0) s_red[it][grp][gw] = make_float2(c1, c2);
+      if ((lane & 15) == 0) reinterpret_cast<float*>(&s_red[it][grp][gw])[lane >> 4] = c1;
       bar_sync_n(1 + grp, T);  // one barrier a row: s_red[it] is written again only after the next row's barrier
       c1 = c2 = 0.0f;
       for (int i = 0; i < nw; i += 2) {
@@ -486,14 +496,16 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
         c1 += v.x + v.z;
         c2 += v.y + v.w;
       }
+    } else {
+      c2 = __shfl_sync(0xffffffffu, c1, 16);
+      c1 = __shfl_sync(0xffffffffu, c1, 0);
     }
     c1 *= inv_k;
     c2 *= inv_k;
     if (!kLayer) {
-      rstd = __fdiv_rn(1.0f, __fsqrt_rn(c1 + a.eps));
-      c2 *= rstd * rstd;  // against x instead of xh
+      rstd = rsqrtf(c1 + a.eps);  // within 2 ulp, as good as the sums
+      c2 *= rstd * rstd;          // against x instead of xh
     }
-    uint16_t* dxr = a.dx + row * K;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int c = t + j * T;
@@ -510,8 +522,13 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
         if (kLayer) dbv[j][i] = __fadd2_rn(dbv[j][i], yf[j][i]);
         o[i] = pack_bf16x2(s.x, s.y);
       }
-      if (c < chunks) store8_bf16(dxr, 8 * c, K, vdx, o);
+      if (kFast) {
+        if (j < G - 1 || c < chunks) *reinterpret_cast<uint4*>(pd + 8 * j * T) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else if (c < chunks) {
+        store8_bf16(pd - 8 * t, 8 * c, K, vdx, o);
+      }
     }
+    pd += sd;
   }
   pdl_launch_dependents();
   // the groups' column sums, added in order of the groups; the last writes the CTA's partial row
