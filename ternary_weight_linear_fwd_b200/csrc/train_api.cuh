@@ -193,6 +193,11 @@ GgPlan gg_plan(int64_t rows, int cols, int red, double kb, int sm_count) {
   return p;
 }
 
+// dW: 0.53 us a k-block with expansion; long reductions run without (bw_dense), 0.38.
+GgPlan bw_plan(int N, int K, int M, int sm_count) {
+  return gg_plan(N, K, M, M > kGgChunk * kGgRed ? 0.38 : 0.53, sm_count);
+}
+
 size_t gg_slab_bytes(const GgPlan& p) {
   return static_cast<size_t>(p.units - p.full) * kGgSlab * 4;
 }
@@ -240,7 +245,11 @@ GgLayout gg_layout(const GgPlan& p, int64_t M, int64_t N, int64_t lddy, size_t b
   return l;
 }
 
-bool bw_dense(const GgPlan& p, int64_t M, int K) { return gg_dense(p, 0.14, M * K, 3.0); }
+// dW also where a part is longer than one sum in TMEM may be: only the kernel without expansion has registers to add up
+// several.
+bool bw_dense(const GgPlan& p, int64_t M, int K) {
+  return (p.full ? p.kblocks : p.per) > kGgChunk || gg_dense(p, 0.14, M * K, 3.0);
+}
 bool bi_dense(const GgPlan& p, int64_t N, int K) { return gg_dense(p, 0.06, N * K, 2.25); }
 size_t bw_b_bytes(const GgPlan& p, int64_t M, int K, int64_t ldq) {
   return bw_dense(p, M, K) ? static_cast<size_t>(M) * k16(K) * 2 : ldq % 16 ? static_cast<size_t>(M) * k16(K) : 0;
@@ -514,7 +523,7 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
 
 size_t bitlinear_backward_weight_workspace_bytes(int32_t M, int32_t N, int32_t K, int64_t lddy, int64_t ldq) {
   if (check_nk(N, K) != BITLINEAR_OK || M < 1 || M > BITLINEAR_MAX_M || lddy < N || ldq < K) return 0;
-  const GgPlan p = gg_plan(N, K, M, 0.53, plan_sm_count());
+  const GgPlan p = bw_plan(N, K, M, plan_sm_count());
   return gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq)).total;
 }
 
@@ -533,7 +542,7 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const GgPlan p = gg_plan(N, K, M, 0.53, dev->sm_count);
+  const GgPlan p = bw_plan(N, K, M, dev->sm_count);
   const GgLayout l = gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq));
   if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -562,11 +571,8 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   a.dw = dW;
   a.accumulate = (flags & BITLINEAR_FLAG_ACCUMULATE) != 0;
   a.vec = K % 8 == 0 && aligned32(dW);
-  // Stores by TMA go through shared memory, which the MMAs of the next tile need: 16 x 2560 x 6912 took 19.5 us with a
-  // row a lane (32 lines an instruction) and 15.4 by TMA, but 4096 x 11008 x 2048 132 and 140.  So TMA where no next
-  // tile's k-blocks run beside the stores or only a few do, where it saves the reads of an accumulation, and for rows
-  // that 32-byte stores cannot take.
-  a.tma = K % 4 == 0 && aligned16(dW) && (a.accumulate || !a.vec || p.units <= p.pairs || p.kblocks <= 8);
+  // by TMA: a row a lane writes 32 lines an instruction (16 x 2560 x 6912: 19.5 us against 15.4)
+  a.tma = K % 4 == 0 && aligned16(dW);
   CUtensorMap mC = mA;
   if (a.tma && !make_map(&mC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dW, K, N, 4 * static_cast<uint64_t>(K), 32, 32, 128))
     return BITLINEAR_ERR_CUDA;

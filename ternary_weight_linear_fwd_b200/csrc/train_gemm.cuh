@@ -48,6 +48,10 @@ constexpr int kGgCols = 256;      // columns of a pair tile (128 of B a CTA)
 constexpr int kGgRed = 64;        // steps of the reduction per stage
 constexpr int kGgStoring = 8;      // storing warps, two for each 32 rows: one waits for memory while the other computes
 constexpr int kGgGroups = 2;       // groups of four expanding warps, taking the stages in turn
+// dW: k-blocks (12: 768 tokens) that are summed in TMEM.  The tensor cores cut every addition off below its last place,
+// always towards zero, so the error of a sum grows with its length (relative, 777 tokens 6e-7, 2048 1.7e-6, 8192 7e-6);
+// longer reductions are added up from pieces of this length in registers, rounded to nearest (7e-7 at any length).
+constexpr int kGgChunk = 12;
 constexpr int kGgSlab = kGgRows * kGgCols;  // fp32 of one part of a split tile
 
 struct GradArgs {
@@ -78,6 +82,8 @@ struct GG {
   static constexpr int S = kWeight && !kDense ? 5 : 6;
   static constexpr int R = kDense ? S : 4;          // S >= R: an operand slot's wait is on the stage that filled it
   static constexpr int GROUPS = kDense ? 0 : kGgGroups;
+  // k-blocks of one sum in TMEM; dW without kDense is given no longer ones, and dx is rounded to bf16
+  static constexpr int CHUNK = kWeight && kDense ? kGgChunk : 1 << 30;
   static constexpr int THREADS = 32 * (4 + 4 * GROUPS + kGgStoring);
   static constexpr int OUT = kGgStoring * 4096;     // a 32 x 32 tile of results for each storing warp
   static constexpr int FIXED = OUT + 512;
@@ -327,38 +333,40 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
       // ------------------------------------------------------------ MMAs (rank 0 only)
       bool issued = false, ok = true;
       int i = 0, t = 0;
-      for (int g = pair; g < a.units && ok; g += npairs, ++t) {
+      for (int g = pair; g < a.units && ok; g += npairs) {
         int row0, col0, kb0;
         const int n = unit_of(g, row0, col0, kb0);
-        const int buf = t & 1;
-        if (t >= 2 && !mbar_wait_cluster(&accempty[buf], ((t >> 1) - 1) & 1)) {
-          *a.status = kDevTimeoutMma;
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t dcol = tmem + buf * kGgCols;
-        for (int kb = 0; kb < n; ++kb, ++i) {
-          const int s = i % S, j = i % R;
-          // both CTAs' expanding warps arrived: both copies landed and both operands are written
-          if (!mbar_wait_cluster(&opready[j], (i / R) & 1)) {
+        for (int k0 = 0; k0 < n && ok; k0 += C::CHUNK, ++t) {
+          const int buf = t & 1;
+          if (t >= 2 && !mbar_wait_cluster(&accempty[buf], ((t >> 1) - 1) & 1)) {
             *a.status = kDevTimeoutMma;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ua = smem_u32(sA + s * C::A_STAGE), ub = smem_u32(sOp + j * C::OP);
+          const uint32_t dcol = tmem + buf * kGgCols;
+          for (int kb = k0; kb < min(n, k0 + C::CHUNK); ++kb, ++i) {
+            const int s = i % S, j = i % R;
+            // both CTAs' expanding warps arrived: both copies landed and both operands are written
+            if (!mbar_wait_cluster(&opready[j], (i / R) & 1)) {
+              *a.status = kDevTimeoutMma;
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t ua = smem_u32(sA + s * C::A_STAGE), ub = smem_u32(sOp + j * C::OP);
 #pragma unroll
-          for (int kk = 0; kk < kGgRed / 16; ++kk) {
-            const uint64_t ad = kWeight ? smem_desc_sw128_mnmajor(ua + kk * 2048, 8192)
-                                        : smem_desc_sw128_kmajor(ua) + static_cast<uint64_t>(kk * 2);
-            tc_mma_f16_ss_pair(dcol, ad, smem_desc_sw128_mnmajor(ub + kk * 2048, 8192), C::IDESC,
-                               (kb | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < kGgRed / 16; ++kk) {
+              const uint64_t ad = kWeight ? smem_desc_sw128_mnmajor(ua + kk * 2048, 8192)
+                                          : smem_desc_sw128_kmajor(ua) + static_cast<uint64_t>(kk * 2);
+              tc_mma_f16_ss_pair(dcol, ad, smem_desc_sw128_mnmajor(ub + kk * 2048, 8192), C::IDESC,
+                                 kb != k0 || kk != 0 ? 1u : 0u);
+            }
+            tc_commit_pair_mc(&empty[s], 0x3);  // frees copy stage s, and operand slot j for k-block i + R
+            issued = true;
           }
-          tc_commit_pair_mc(&empty[s], 0x3);  // frees copy stage s, and operand slot j for k-block i + R
-          issued = true;
+          if (ok) tc_commit_pair_mc(&accfull[buf], 0x3);
         }
-        if (ok) tc_commit_pair_mc(&accfull[buf], 0x3);
       }
       if (!ok && issued) {
         tc_commit_pair(drain);
@@ -454,77 +462,108 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     const int q = warp & 3, first = ((warp - 4 - 4 * G) >> 2) * 32;  // 32 rows, every other 32 columns
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float alpha = kWeight ? 1.0f : *a.alpha;
-    // dW's plain stores beside the next tile's k-blocks are left to the first four warps (2048 x 2560 x 6912: 61.4 us
-    // against 65 with all eight)
-    const bool solo = kWeight && !a.tma;
-    const int step = solo ? 32 : 64;
-    int t = 0;
-    for (int g = pair; g < a.units; g += npairs, ++t) {
-      const int buf = t & 1;
-      int row0, col0, kb0;
-      unit_of(g, row0, col0, kb0);
-      const int wrow = static_cast<int>(rank) * 128 + q * 32;  // the warp's first row of the tile
+    // 32 columns of a row a lane, from c0 of the tile: to their slab, or finished
+    auto finish = [&](int g, int row0, int col0, int wrow, int c0, const float (&v)[32], const uint32_t (&s0)[16]) {
       const bool part = g >= a.full && a.split > 1;
       float* out = sOut + (warp - 4 - 4 * G) * 1024;
-      uint32_t s0[16], s1[16];
-      if (!kWeight && !part) grad_addend<false, 32>(a, row0 + wrow + lane, col0 + first, s0);
-      if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
-        *a.status = kDevTimeoutEpilogue;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll 1
-      for (int c0 = solo && first ? kGgCols : first; c0 < kGgCols; c0 += step) {
-        uint32_t w[32];
-        tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
-        if (!kWeight && !part && c0 + step < kGgCols)
-          grad_addend<false, 32>(a, row0 + wrow + lane, col0 + c0 + step, s1);
-        tc_wait_ld();
-        float v[32];
+      if (row0 + wrow < a.rows && col0 + c0 < a.cols) {
+        if (part) {
+          float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + wrow + lane) * 8;
 #pragma unroll
-        for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
-          v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
-        if (row0 + wrow < a.rows && col0 + c0 < a.cols) {
-          if (part) {
-            float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + wrow + lane) * 8;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) st_global_v8(p + c * 8 * kGgRows, reinterpret_cast<const uint32_t*>(v + 8 * c));
-          } else if (!kWeight && a.vec && col0 + c0 + 32 <= a.cols) {
-            if (row0 + wrow + lane < a.rows)
-              grad_store<false, 32>(a, row0 + wrow + lane, col0 + c0, v, s0, alpha);
-          } else if (kWeight && a.tma) {
-            if (lane == 0) bulk_wait_read<0>();  // the last store has read the tile
-            __syncwarp();
-            grad_tile_put(out, v);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (a.accumulate)
-                tma_add_2d(&mapC, col0 + c0, row0 + wrow, out);
-              else
-                tma_store_2d(&mapC, col0 + c0, row0 + wrow, out);
-              bulk_commit();
-            }
-          } else if (kWeight && a.vec && !a.accumulate && col0 + c0 + 32 <= a.cols) {
-            if (row0 + wrow + lane < a.rows) {
-              float* p = a.dw + static_cast<int64_t>(row0 + wrow + lane) * a.cols + col0 + c0;
-#pragma unroll
-              for (int c = 0; c < 32; c += 8) st_global_v8(p + c, reinterpret_cast<const uint32_t*>(v + c));
-            }
-          } else {
-            grad_tile_put(out, v);
-            __syncwarp();
-            grad_store_tile<kWeight>(a, row0 + wrow, col0 + c0, out, alpha);
-            __syncwarp();
+          for (int c = 0; c < 4; ++c) st_global_v8(p + c * 8 * kGgRows, reinterpret_cast<const uint32_t*>(v + 8 * c));
+        } else if (!kWeight && a.vec && col0 + c0 + 32 <= a.cols) {
+          if (row0 + wrow + lane < a.rows)
+            grad_store<false, 32>(a, row0 + wrow + lane, col0 + c0, v, s0, alpha);
+        } else if (kWeight && a.tma) {
+          if (lane == 0) bulk_wait_read<0>();  // the last store has read the tile
+          __syncwarp();
+          grad_tile_put(out, v);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (a.accumulate)
+              tma_add_2d(&mapC, col0 + c0, row0 + wrow, out);
+            else
+              tma_store_2d(&mapC, col0 + c0, row0 + wrow, out);
+            bulk_commit();
           }
+        } else {
+          grad_tile_put(out, v);
+          __syncwarp();
+          grad_store_tile<kWeight>(a, row0 + wrow, col0 + c0, out, alpha);
+          __syncwarp();
         }
-        if (!kWeight)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s0[i] = s1[i];
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote_cta(accempty0 + static_cast<uint32_t>(buf * 8));
+    };
+    int t = 0;
+    for (int g = pair; g < a.units; g += npairs) {
+      int row0, col0, kb0;
+      const int n = unit_of(g, row0, col0, kb0);
+      const int wrow = static_cast<int>(rank) * 128 + q * 32;  // the warp's first row of the tile
+      if constexpr (C::CHUNK < 1 << 30) {
+        // the warp's 32 rows of 4 x 32 columns are summed up in registers, then stored while the next tile is computed
+        float acc[4][32];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) acc[u][c] = 0.0f;
+        bool ok = true;
+        for (int k0 = 0; k0 < n; k0 += C::CHUNK, ++t) {
+          const int buf = t & 1;
+          if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
+            *a.status = kDevTimeoutEpilogue;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t w[16];
+            tc_ld_32x32b_x16(tmem + lane_base + buf * kGgCols + first + 64 * (u / 2) + 16 * (u % 2), w);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              acc[u / 2][16 * (u % 2) + c] = __fadd_rn(acc[u / 2][16 * (u % 2) + c], __uint_as_float(w[c]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_cta(accempty0 + static_cast<uint32_t>(buf * 8));
+        }
+        if (!ok) break;
+        const uint32_t none[16] = {};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) finish(g, row0, col0, wrow, first + 64 * u, acc[u], none);
+      } else {
+        const int buf = t & 1;
+        const bool part = g >= a.full && a.split > 1;
+        uint32_t s0[16], s1[16];
+        if (!kWeight && !part) grad_addend<false, 32>(a, row0 + wrow + lane, col0 + first, s0);
+        if (!mbar_wait(&accfull[buf], (t >> 1) & 1)) {
+          *a.status = kDevTimeoutEpilogue;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = first; c0 < kGgCols; c0 += 64) {
+          uint32_t w[32];
+          tc_ld_32x32b_x32(tmem + lane_base + buf * kGgCols + c0, w);
+          if (!kWeight && !part && c0 + 64 < kGgCols)
+            grad_addend<false, 32>(a, row0 + wrow + lane, col0 + c0 + 64, s1);
+          tc_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c)  // 2-bit rows: accumulator column 2 i + h of a 16-group is output column i + 8 h
+            v[kWeight || kDense ? c : (c & 16) + ((c & 15) >> 1) + 8 * (c & 1)] = __uint_as_float(w[c]);
+          finish(g, row0, col0, wrow, c0, v, s0);
+          if (!kWeight)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s0[i] = s1[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_cta(accempty0 + static_cast<uint32_t>(buf * 8));
+        ++t;
+      }
     }
     if (kWeight && lane == 0) bulk_wait<0>();  // results are in memory before the CTA ends
   }
