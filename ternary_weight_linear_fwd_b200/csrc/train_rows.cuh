@@ -16,6 +16,13 @@ namespace bl {
 
 __device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
 
+// The larger of two, NaN if either is: a row's maximum must not hide one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 8 fp32 parameters from k0 (zero past K); one 32-byte load where p is 32-byte aligned.
 __device__ __forceinline__ void load8_f32(const float* p, int k0, int K, bool vec, float2 (&v)[4]) {
   if (vec && k0 + 8 <= K) {
@@ -281,14 +288,14 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
     normed(kRegs ? min(c, chunks - 1) : c, r, xn);
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(xn[i].x), fabsf(xn[i].y)));
-    mx = c < chunks ? fmaxf(mx, m) : mx;
+    for (int i = 0; i < 4; ++i) m = max_nan(m, max_nan(fabsf(xn[i].x), fabsf(xn[i].y)));
+    mx = c < chunks ? max_nan(mx, m) : mx;
   });
   mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
   if (wpr > 1) {
     if (lane == 0) s_mx[warp] = mx;
     __syncthreads();
-    for (int i = 0; i < wpr; ++i) mx = fmaxf(mx, s_mx[rloc * wpr + i]);
+    for (int i = 0; i < wpr; ++i) mx = max_nan(mx, s_mx[rloc * wpr + i]);
   }
   const float d = __fadd_rn(mx, kEps);
   const float c127 = __fmul_rn(kQb, __frcp_rn(d));

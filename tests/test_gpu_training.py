@@ -658,3 +658,64 @@ def test_backward_input_restored_operand(n, m, M, N, K):
         T *= torch.zeros_like(blocks).scatter_(2, blocks.abs().argsort(dim=2, descending=True, stable=True)[:, :, :n],
                                                1).view(N, K)
     _check_input(w, T.to(torch.int8), _rand(M + N, M, N, scale=1e-3), _rand(M, M, K, scale=1e-3))
+
+
+# ---------------------------------------------------------------- rows that are not numbers
+@pytest.mark.parametrize("K", [16, 203, 2560, 11008])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_layernorm_keeps_nan(K, bad):
+    """A row with a NaN or an infinity has no mean: its output, row maximum and restored values are NaN; others stay."""
+    x = _rand(K, 9, K)
+    y = x.clone()
+    y[4, K // 2] = bad
+    w, b = torch.rand(K, device=DEV) + 0.5, torch.rand(K, device=DEV)
+    keep = [0, 1, 2, 3, 5, 6, 7, 8]
+    out, clean = bl.layernorm(y, w, b), bl.layernorm(x, w, b)
+    assert bool(out[4].isnan().all()) and torch.equal(out[keep], clean[keep])
+    q, gamma, rs = bl.layernorm_quant_act(y, w, b)
+    q0, gamma0, rs0 = bl.layernorm_quant_act(x, w, b)
+    assert bool(gamma[4].isnan()) and bool(bl.dequant_act(q, gamma)[4].isnan().all())
+    assert torch.equal(q[keep], q0[keep]) and torch.equal(gamma[keep], gamma0[keep]) and torch.equal(rs[keep], rs0[keep])
+
+
+@pytest.mark.parametrize("N", [16, 203, 6912])
+def test_checkpoint_keeps_nan(N):
+    g, u = _rand(N, 5, N), _rand(N + 1, 5, N)
+    g[2, N - 1] = float("nan")
+    u[3, 0] = float("nan")
+    c = bl.relu2_glu_quant_act(g, u)
+    assert bool(c.gamma_g[2].isnan()) and bool(c.gamma_u[3].isnan())
+    dg, du = bl.relu2_glu_backward(_rand(N + 2, 5, N), c.q_g, c.gamma_g, c.q_u, c.gamma_u)
+    assert bool(dg[3].isnan().any()) and bool(torch.isfinite(dg[[0, 1, 4]].float()).all())
+    assert bool(torch.isfinite(du[[0, 1, 4]].float()).all())
+
+
+def test_norm_backward_nan_stays_in_its_row():
+    M, K = 30, 2560
+    x, dy = _rand(1, M, K), _rand(2, M, K)
+    w = torch.rand(K, device=DEV)
+    mean, rstd = _moments(x, 1e-5)
+    dx, _, _ = bl.layernorm_backward(dy, x, w, mean, rstd)
+    dy2 = dy.clone()
+    dy2[7, 5] = float("nan")
+    dx2, dw2, db2 = bl.layernorm_backward(dy2, x, w, mean, rstd)
+    keep = [i for i in range(M) if i != 7]
+    assert torch.equal(dx2[keep], dx[keep]) and bool(dx2[7].isnan().all())
+    assert bool(dw2[5].isnan()) and int(dw2.isnan().sum()) == 1 and int(db2.isnan().sum()) == 1
+
+
+def test_product_nan_stays_in_its_row():
+    """A NaN in one row of dy reaches only that row of dx (few tokens and many) and, in one column, only that row of dW."""
+    for M, N, K in [(20, 300, 200), (700, 300, 2048), (5000, 2560, 2560)]:
+        w = bl.pack_ternary(torch.randint(-1, 2, (N, K), device=DEV, dtype=torch.int8, generator=_gen(1)), 0.02)
+        dy = _rand(2, M, N)
+        q, gamma = _checkpoint(3, M, K)
+        dx, dW = bl.backward_input(w, dy), bl.backward_weight(dy, q, gamma)
+        bad = dy.clone()
+        bad[M // 3, 77] = float("nan")
+        keep = [i for i in range(M) if i != M // 3]
+        dx2 = bl.backward_input(w, bad)
+        assert torch.equal(dx2[keep], dx[keep]) and bool(dx2[M // 3].isnan().all())
+        dW2 = bl.backward_weight(bad, q, gamma)
+        rows = [i for i in range(N) if i != 77]
+        assert torch.equal(dW2[rows], dW[rows]) and bool(dW2[77].isnan().all())
