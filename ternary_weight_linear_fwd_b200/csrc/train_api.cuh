@@ -145,8 +145,19 @@ bitlinear_status check_norm_backward(const NbArgs& a, const float* dw, const flo
   return BITLINEAR_OK;
 }
 
+// Chunks of 16 of an M x K matrix for the flat kernels (32-bit counts), 0 where they do not apply.
+int64_t flat_chunks(int M, int K) {
+  const int64_t n = static_cast<int64_t>(M) * (K / 16);
+  return K % 16 == 0 && n < (1ll << 31) ? n : 0;
+}
+
 bitlinear_status dequant_launch(const int8_t* q, int64_t ldq, const float* gamma, int M, int K, uint16_t* y,
                                 int64_t ldy, cudaStream_t s, bool pdl, int sm_count) {
+  const int64_t total = flat_chunks(M, K);
+  if (total > 0 && ldq == K && ldy == K && aligned16(q) && aligned32(y))
+    return launch(dequant_flat_kernel, dim3(static_cast<unsigned>((total + 256 * kFlatChunks - 1) / (256 * kFlatChunks))),
+                  dim3(256), 0, s, pdl, reinterpret_cast<const uint4*>(q), gamma, static_cast<uint32_t>(K / 16),
+                  static_cast<uint32_t>(total), y);
   const int lanes = row_lanes(M, K, 8, sm_count), rpc = 256 / lanes;
   return launch(dequant_act_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, s, pdl, q, ldq, gamma, M, K, y, ldy, lanes);
 }
@@ -514,9 +525,17 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
-  const int lanes = row_lanes(M, N, 4, dev->sm_count), rpc = 256 / lanes;
-  st = launch(relu2_glu_backward_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, static_cast<cudaStream_t>(stream),
-              false, dh, lddh, q_g, gamma_g, q_u, gamma_u, M, N, dg, du, lanes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t total = flat_chunks(M, N);
+  if (total > 0 && lddh == N && aligned32(dh) && aligned16(q_g) && aligned16(q_u) && aligned32(dg) && aligned32(du)) {
+    st = launch(relu2_glu_backward_flat_kernel, dim3(static_cast<unsigned>((total + 511) / 512)), dim3(256), 0, s, false,
+                dh, reinterpret_cast<const uint4*>(q_g), gamma_g, reinterpret_cast<const uint4*>(q_u), gamma_u,
+                static_cast<uint32_t>(N / 16), static_cast<uint32_t>(total), dg, du);
+  } else {
+    const int lanes = row_lanes(M, N, 4, dev->sm_count), rpc = 256 / lanes;
+    st = launch(relu2_glu_backward_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, s, false, dh, lddh, q_g, gamma_g,
+                q_u, gamma_u, M, N, dg, du, lanes);
+  }
   if (st == BITLINEAR_OK) t_last_kernel = "relu2_glu_backward";
   return st;
 }
