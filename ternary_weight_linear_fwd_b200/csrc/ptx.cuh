@@ -158,14 +158,10 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, int32_t x, in
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// At most kLeft groups still read shared memory (bulk_wait_read) or are incomplete (bulk_wait).
+// At most kLeft groups of this thread still read shared memory.
 template <int kLeft>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
-}
-template <int kLeft>
-__device__ __forceinline__ void bulk_wait() {
-  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 

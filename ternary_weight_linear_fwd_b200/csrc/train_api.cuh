@@ -206,7 +206,7 @@ GgPlan gg_plan(int64_t rows, int cols, int red, double kb, int sm_count) {
 
 // dW: 0.53 us a k-block with expansion; long reductions run without (bw_dense), 0.38.
 GgPlan bw_plan(int N, int K, int M, int sm_count) {
-  return gg_plan(N, K, M, M > kGgChunk * kGgRed ? 0.38 : 0.53, sm_count);
+  return gg_plan(N, K, M, M > kGgOneSum * kGgRed ? 0.38 : 0.53, sm_count);
 }
 
 size_t gg_slab_bytes(const GgPlan& p) {
@@ -259,7 +259,7 @@ GgLayout gg_layout(const GgPlan& p, int64_t M, int64_t N, int64_t lddy, size_t b
 // dW also where a part is longer than one sum in TMEM may be: only the kernel without expansion has registers to add up
 // several.
 bool bw_dense(const GgPlan& p, int64_t M, int K) {
-  return (p.full ? p.kblocks : p.per) > kGgChunk || gg_dense(p, 0.14, M * K, 3.0);
+  return (p.full ? p.kblocks : p.per) > kGgOneSum || gg_dense(p, 0.14, M * K, 3.0);
 }
 bool bi_dense(const GgPlan& p, int64_t N, int K) { return gg_dense(p, 0.06, N * K, 2.25); }
 size_t bw_b_bytes(const GgPlan& p, int64_t M, int K, int64_t ldq) {

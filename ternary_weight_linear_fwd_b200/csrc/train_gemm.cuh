@@ -52,6 +52,7 @@ constexpr int kGgGroups = 2;       // groups of four expanding warps, taking the
 // always towards zero, so the error of a sum grows with its length (relative, 777 tokens 6e-7, 2048 1.7e-6, 8192 7e-6);
 // longer reductions are added up from pieces of this length in registers, rounded to nearest (7e-7 at any length).
 constexpr int kGgChunk = 12;
+constexpr int kGgOneSum = 14;  // reductions up to this long (896 tokens, 8e-7) may stay one sum: the kernel with expansion
 constexpr int kGgSlab = kGgRows * kGgCols;  // fp32 of one part of a split tile
 
 struct GradArgs {
@@ -82,7 +83,7 @@ struct GG {
   static constexpr int S = kWeight && !kDense ? 5 : 6;
   static constexpr int R = kDense ? S : 4;          // S >= R: an operand slot's wait is on the stage that filled it
   static constexpr int GROUPS = kDense ? 0 : kGgGroups;
-  // k-blocks of one sum in TMEM; dW without kDense is given no longer ones, and dx is rounded to bf16
+  // k-blocks of one sum in TMEM; dW without kDense is given at most kGgOneSum, and dx is rounded to bf16
   static constexpr int CHUNK = kWeight && kDense ? kGgChunk : 1 << 30;
   static constexpr int THREADS = 32 * (4 + 4 * GROUPS + kGgStoring);
   static constexpr int OUT = kGgStoring * 4096;     // a 32 x 32 tile of results for each storing warp
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     fence_mbar_init();
     tma_prefetch_desc(&mapA);
     tma_prefetch_desc(&mapB);
+    if (kWeight && a.tma) tma_prefetch_desc(&mapC);
   }
   if (warp == 2) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
         ++t;
       }
     }
-    if (kWeight && lane == 0) bulk_wait<0>();  // results are in memory before the CTA ends
+    if (kWeight && lane == 0) bulk_wait_read<0>();  // the stores have read the tiles before the CTA ends
   }
   tc_fence_before();
   __syncthreads();
