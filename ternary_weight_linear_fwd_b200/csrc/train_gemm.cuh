@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], C::A_STAGE + C::RAW);
+          mbar_arrive_expect_tx(&full[s], C::A_STAGE + C::RAW + test_extra_tx());
           uint8_t* dA = sA + s * C::A_STAGE;
           if (kWeight) {
             tma_load_2d(dA, &mapA, 2 * row0, kb * kGgRed, &full[s]);
