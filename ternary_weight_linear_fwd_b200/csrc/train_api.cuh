@@ -52,19 +52,27 @@ bitlinear_status layernorm_launch(LnArgs a, cudaStream_t s, int sm_count) {
   a.lw = log2i(wpr);
   a.inv_k = 1.0 / a.K;
   const bool fast = rows16(a.x, a.ldx, a.K) && aligned32(a.w) && aligned32(a.b) && aligned16(a.y) && aligned8(a.q);
-  const int need = fast ? row_chunks(a.K, wpr) : kLnMaxChunks + 1;
+  const int need = row_chunks(a.K, wpr);
   const int rpc = kQuantWarps / wpr;
   const dim3 grid((a.M + rpc - 1) / rpc), block(32 * kQuantWarps);
   auto go = [&](auto kern) { return launch(kern, grid, block, 0, s, false, a); };
-  if (need <= 1) return go(layernorm_kernel<kCodes, 1>);
-  if (need <= 2) return go(layernorm_kernel<kCodes, 2>);
-  if (need <= 3) return go(layernorm_kernel<kCodes, 3>);
-  if (need <= 4) return go(layernorm_kernel<kCodes, 4>);
-  if (need <= 5) return go(layernorm_kernel<kCodes, 5>);
-  if (need <= 6) return go(layernorm_kernel<kCodes, 6>);
-  if (need <= 8) return go(layernorm_kernel<kCodes, 8>);
-  if (need <= kLnMaxChunks) return go(layernorm_kernel<kCodes, kLnMaxChunks>);
-  return go(layernorm_kernel<kCodes, 0>);
+  if (need > kLnMaxChunks)
+    return fast ? go(layernorm_kernel<kCodes, false, 0>) : go(layernorm_kernel<kCodes, true, 0>);
+  if (fast) {
+    if (need <= 1) return go(layernorm_kernel<kCodes, false, 1>);
+    if (need <= 2) return go(layernorm_kernel<kCodes, false, 2>);
+    if (need <= 3) return go(layernorm_kernel<kCodes, false, 3>);
+    if (need <= 4) return go(layernorm_kernel<kCodes, false, 4>);
+    if (need <= 5) return go(layernorm_kernel<kCodes, false, 5>);
+    if (need <= 6) return go(layernorm_kernel<kCodes, false, 6>);
+    if (need <= 8) return go(layernorm_kernel<kCodes, false, 8>);
+    return go(layernorm_kernel<kCodes, false, kLnMaxChunks>);
+  }
+  if (need <= 1) return go(layernorm_kernel<kCodes, true, 1>);
+  if (need <= 2) return go(layernorm_kernel<kCodes, true, 2>);
+  if (need <= 4) return go(layernorm_kernel<kCodes, true, 4>);
+  if (need <= 6) return go(layernorm_kernel<kCodes, true, 6>);
+  return go(layernorm_kernel<kCodes, true, kLnMaxChunks>);
 }
 
 bitlinear_status check_layernorm(const LnArgs& a) {
@@ -145,19 +153,18 @@ bitlinear_status check_norm_backward(const NbArgs& a, const float* dw, const flo
   return BITLINEAR_OK;
 }
 
-// Chunks of 16 of an M x K matrix for the flat kernels (32-bit counts), 0 where they do not apply.
-int64_t flat_chunks(int M, int K) {
-  const int64_t n = static_cast<int64_t>(M) * (K / 16);
-  return K % 16 == 0 && n < (1ll << 31) ? n : 0;
+// Elements of a contiguous M x K matrix for the flat kernels (32-bit counts), 0 where they do not apply.
+uint32_t flat_count(int M, int K) {
+  const int64_t n = static_cast<int64_t>(M) * K;
+  return K >= 16 && n < (1ll << 32) - 65536 ? static_cast<uint32_t>(n) : 0u;
 }
 
 bitlinear_status dequant_launch(const int8_t* q, int64_t ldq, const float* gamma, int M, int K, uint16_t* y,
                                 int64_t ldy, cudaStream_t s, bool pdl, int sm_count) {
-  const int64_t total = flat_chunks(M, K);
-  if (total > 0 && ldq == K && ldy == K && aligned16(q) && aligned32(y))
-    return launch(dequant_flat_kernel, dim3(static_cast<unsigned>((total + 256 * kFlatChunks - 1) / (256 * kFlatChunks))),
-                  dim3(256), 0, s, pdl, reinterpret_cast<const uint4*>(q), gamma, static_cast<uint32_t>(K / 16),
-                  static_cast<uint32_t>(total), y);
+  const uint32_t count = flat_count(M, K), per = 16 * 256 * kFlatChunks;
+  if (count > 0 && ldq == K && ldy == K && aligned16(q) && aligned32(y))
+    return launch(dequant_flat_kernel, dim3((count / 16 * 16 + per - 1) / per), dim3(256), 0, s, pdl, q, gamma,
+                  static_cast<uint32_t>(K), count, y);
   const int lanes = row_lanes(M, K, 8, sm_count), rpc = 256 / lanes;
   return launch(dequant_act_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, s, pdl, q, ldq, gamma, M, K, y, ldy, lanes);
 }
@@ -496,19 +503,26 @@ bitlinear_status bitlinear_relu2_glu_quant_act(const uint16_t* g, int64_t ldg, c
   const int wpr = row_warps(M, N, kGluMaxChunks, dev->sm_count);
   a.lw = log2i(wpr);
   const bool fast = rows16(g, ldg, N) && rows16(u, ldu, N) && aligned8(q_g) && aligned8(q_u) && aligned8(q_h);
-  const int need = fast ? row_chunks(N, wpr) : kGluMaxChunks + 1;
+  const int need = row_chunks(N, wpr);
   const int rpc = kQuantWarps / wpr;
   auto go = [&](auto kern) {
     return launch(kern, dim3((M + rpc - 1) / rpc), dim3(32 * kQuantWarps), 0, static_cast<cudaStream_t>(stream), false,
                   a);
   };
-  st = need <= 1                ? go(relu2_glu_quant_kernel<1>)
-       : need <= 2              ? go(relu2_glu_quant_kernel<2>)
-       : need <= 3              ? go(relu2_glu_quant_kernel<3>)
-       : need <= 4              ? go(relu2_glu_quant_kernel<4>)
-       : need <= 5              ? go(relu2_glu_quant_kernel<5>)
-       : need <= kGluMaxChunks  ? go(relu2_glu_quant_kernel<kGluMaxChunks>)
-                                : go(relu2_glu_quant_kernel<0>);
+  if (need > kGluMaxChunks)
+    st = fast ? go(relu2_glu_quant_kernel<false, 0>) : go(relu2_glu_quant_kernel<true, 0>);
+  else if (fast)
+    st = need <= 1   ? go(relu2_glu_quant_kernel<false, 1>)
+         : need <= 2 ? go(relu2_glu_quant_kernel<false, 2>)
+         : need <= 3 ? go(relu2_glu_quant_kernel<false, 3>)
+         : need <= 4 ? go(relu2_glu_quant_kernel<false, 4>)
+         : need <= 5 ? go(relu2_glu_quant_kernel<false, 5>)
+                     : go(relu2_glu_quant_kernel<false, kGluMaxChunks>);
+  else
+    st = need <= 1   ? go(relu2_glu_quant_kernel<true, 1>)
+         : need <= 2 ? go(relu2_glu_quant_kernel<true, 2>)
+         : need <= 4 ? go(relu2_glu_quant_kernel<true, 4>)
+                     : go(relu2_glu_quant_kernel<true, kGluMaxChunks>);
   if (st == BITLINEAR_OK) t_last_kernel = "relu2_glu_quant_act";
   return st;
 }
@@ -526,11 +540,11 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
   st = current_device(&dev);
   if (st != BITLINEAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t total = flat_chunks(M, N);
-  if (total > 0 && lddh == N && aligned32(dh) && aligned16(q_g) && aligned16(q_u) && aligned32(dg) && aligned32(du)) {
-    st = launch(relu2_glu_backward_flat_kernel, dim3(static_cast<unsigned>((total + 511) / 512)), dim3(256), 0, s, false,
-                dh, reinterpret_cast<const uint4*>(q_g), gamma_g, reinterpret_cast<const uint4*>(q_u), gamma_u,
-                static_cast<uint32_t>(N / 16), static_cast<uint32_t>(total), dg, du);
+  const uint32_t count = flat_count(M, N);
+  if (count > 0 && lddh == N && aligned32(dh) && aligned16(q_g) && aligned16(q_u) && aligned32(dg) && aligned32(du)) {
+    st = launch(N % 16 ? relu2_glu_backward_flat_kernel<true> : relu2_glu_backward_flat_kernel<false>,
+                dim3((count / 16 + 511) / 512), dim3(256), 0, s, false, dh, q_g, gamma_g, q_u, gamma_u,
+                static_cast<uint32_t>(N), count, dg, du);
   } else {
     const int lanes = row_lanes(M, N, 4, dev->sm_count), rpc = 256 / lanes;
     st = launch(relu2_glu_backward_kernel, dim3((M + rpc - 1) / rpc), dim3(256), 0, s, false, dh, lddh, q_g, gamma_g,

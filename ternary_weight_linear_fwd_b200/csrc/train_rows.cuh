@@ -59,6 +59,51 @@ __device__ __forceinline__ void store8_bf16(uint16_t* row, int k0, int K, bool v
   }
 }
 
+// The same for rows of any alignment, whole words where the address allows.
+__device__ __forceinline__ void store8_bf16_any(uint16_t* row, int k0, int K, const uint32_t* o) {
+  uint16_t* p = row + k0;
+  if (k0 + 8 > K) {
+    store8_bf16(row, k0, K, false, o);
+  } else if ((reinterpret_cast<uintptr_t>(p) & 2u) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(p)[i] = o[i];
+  } else {
+    p[0] = static_cast<uint16_t>(o[0]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(p + 1)[i] = __funnelshift_r(o[i], o[i + 1], 16);
+    p[7] = static_cast<uint16_t>(o[3] >> 16);
+  }
+}
+
+// 8 bf16 values of a row from k0 as 4 words (zero past K), rows of any
+// alignment: the two 16-byte blocks that hold them, shifted into place, unless
+// a block reaches out of the matrix [lo, hi) (its first and last ones).  A row
+// element by element took three to eleven times the aligned one's time.
+__device__ __forceinline__ void load8_any(const uint16_t* row, int k0, int K, const uint16_t* lo, const uint16_t* hi,
+                                          uint32_t (&r)[4]) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(row + k0), a = p & ~static_cast<uintptr_t>(15);
+  const uint32_t s = static_cast<uint32_t>(p & 15u);
+  const uintptr_t b = s ? a + 16 : a;
+  if (a < reinterpret_cast<uintptr_t>(lo) || b + 16 > reinterpret_cast<uintptr_t>(hi)) {
+    load8_raw(row, k0, K, false, r);
+    return;
+  }
+  const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
+  uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  if (s & 8u)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (s & 4u)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (s & 2u) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+  if (k0 + 8 > K) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = k0 + 2 * i >= K ? 0u : k0 + 2 * i + 1 >= K ? r[i] & 0xFFFFu : r[i];
+  }
+}
+
 // 8 codes at row[k0 ..], those past K left out.
 __device__ __forceinline__ void store8_codes(int8_t* row, int k0, int K, bool vec, const uint2 w) {
   if (vec && k0 + 8 <= K) {
@@ -84,6 +129,28 @@ __device__ __forceinline__ void load16_codes(const int8_t* row, int k0, int K, b
         if (k0 + 4 * i + j < K) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k0 + 4 * i + j])) << (8 * j);
     }
   }
+}
+
+// The same for rows of any alignment inside [lo, hi), as load8_any.
+__device__ __forceinline__ void load16_codes_any(const int8_t* row, int k0, int K, const int8_t* lo, const int8_t* hi,
+                                                 uint32_t (&r)[4]) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(row + k0), a = p & ~static_cast<uintptr_t>(15);
+  const uint32_t s = static_cast<uint32_t>(p & 15u);
+  const uintptr_t b = s ? a + 16 : a;
+  if (k0 + 16 > K || a < reinterpret_cast<uintptr_t>(lo) || b + 16 > reinterpret_cast<uintptr_t>(hi)) {
+    load16_codes(row, k0, K, false, r);
+    return;
+  }
+  const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
+  uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  if (s & 8u)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (s & 4u)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(w[i], w[i + 1], 8 * (s & 3u));
 }
 
 // Four int8 codes as fp32, exactly: the code plus 128 goes into the low byte
@@ -163,12 +230,11 @@ struct LnArgs {
 // the row is read once, all its loads in flight together, and with codes its
 // normalised values stay in registers between the maximum and the rounding, so
 // the parameters are read once a row as well (read twice, 16 columns a lane,
-// they filled the L1 pipe for 42 us at 4096 x 2560).  G > 0 needs rows and
-// parameters that 16- and 32-byte loads can take and K % 8 == 0: its steps are
-// loads are free of branches (chunks past K read the last one and are left out
+// they filled the L1 pipe for 42 us at 4096 x 2560).  Without kAny (rows and
+// parameters that 16- and 32-byte loads can take, K % 8 == 0) the (chunks past K read the last one and are left out
 // of sums, maximum and output), so that those of several go out together.
-// G = 0: any row; it is read again for each pass, from L2.
-template <bool kCodes, int G>
+// G = 0: rows longer than any G holds are read again for each pass, from L2.
+template <bool kCodes, bool kAny, int G>
 __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) layernorm_kernel(const LnArgs a) {
   constexpr bool kRegs = G > 0;
   constexpr int GR = kRegs ? G : 1;
@@ -183,9 +249,17 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantWarps >> a.lw) + rloc;
   const bool active = row < a.M;  // inactive warps still reach the CTA barriers
   const uint16_t* xr = a.x + (active ? row : 0) * a.ldx;
-  const bool xvec = kRegs || ((a.ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0);
-  const bool wvec = kRegs || (reinterpret_cast<uintptr_t>(a.w) & 31u) == 0;
-  const bool bvec = kRegs || (reinterpret_cast<uintptr_t>(a.b) & 31u) == 0;
+  const uint16_t* const end = a.x + static_cast<int64_t>(a.M - 1) * a.ldx + K;
+  const bool wvec = !kAny || (reinterpret_cast<uintptr_t>(a.w) & 31u) == 0;
+  const bool bvec = !kAny || (reinterpret_cast<uintptr_t>(a.b) & 31u) == 0;
+  auto load = [&](int c, uint32_t (&r)[4]) {
+    if (kAny) {
+      load8_any(xr, 8 * c, K, a.x, end, r);
+    } else {
+      const uint4 t = *reinterpret_cast<const uint4*>(xr + 8 * c);
+      r[0] = t.x; r[1] = t.y; r[2] = t.z; r[3] = t.w;
+    }
+  };
   const int chunks = (K + 7) / 8;
   const int cstride = 32 * wpr;
   const int c0 = sub * 32 + lane;
@@ -193,11 +267,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
   uint32_t v[GR][4];
   if (kRegs) {
 #pragma unroll
-    for (int j = 0; j < GR; ++j) {
-      const int c = c0 + j * cstride;
-      const uint4 t = *reinterpret_cast<const uint4*>(xr + 8 * min(c, chunks - 1));
-      v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
-    }
+    for (int j = 0; j < GR; ++j) load(min(c0 + j * cstride, chunks - 1), v[j]);
   }
   // f(j, chunk, its words) for each of the lane's chunks, and with G > 0 for those past K too
   auto for_chunks = [&](auto&& f) {
@@ -207,7 +277,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
     } else if (active) {
       for (int c = c0; c < chunks; c += cstride) {
         uint32_t r[4];
-        load8_raw(xr, 8 * c, K, xvec, r);
+        load(c, r);
         f(0, c, r);
       }
     }
@@ -265,8 +335,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
 #pragma unroll
       for (int i = 0; i < 4; ++i) xn[i] = __fadd2_rn(xn[i], b[i]);
   };
-  const bool yvec = kRegs || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0);
-  const bool qvec = kRegs || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 7u) == 0);
+  const bool qvec = !kAny || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 7u) == 0);
 
   if (!kCodes) {
     uint16_t* yr = a.y + (active ? row : 0) * K;
@@ -276,7 +345,11 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(xn[i].x, xn[i].y);
-      if (active && c < chunks) store8_bf16(yr, 8 * c, K, yvec, o);
+      if (!active || c >= chunks) return;
+      if (kAny)
+        store8_bf16_any(yr, 8 * c, K, o);
+      else
+        *reinterpret_cast<uint4*>(yr + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
     });
     return;
   }
@@ -302,14 +375,15 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
   int32_t sum = 0;
   uint32_t redo = 0u;  // chunks whose codes take the exact quotient
   int8_t* qr = a.q + (active ? row : 0) * K;
-  auto exact = [&](int c, const uint2 w0) {  // replaces w0, the chunk's codes
+  auto exact = [&](int c) {  // replaces the chunk's codes
     uint32_t r[4];
     float2 xn[4];
-    load8_raw(xr, 8 * c, K, xvec, r);
+    load(c, r);
     normed(c, r, xn);
+    float emax = 0.0f;
     const uint2 w = codes8_exact(xn, d);
+    sum += code_sum(w) - code_sum(codes8_near(xn, c127, emax));
     store8_codes(qr, 8 * c, K, qvec, w);
-    sum += code_sum(w) - code_sum(w0);
   };
   for_chunks([&](int j, int c, const uint32_t (&r)[4]) {
     float2(&xn)[4] = xs[kCodes ? j : 0];
@@ -323,13 +397,13 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
       if (kRegs)
         redo |= 1u << j;
       else
-        exact(c, w);
+        exact(c);
     }
   });
   while (kRegs && redo) {
     const int c = c0 + (__ffs(redo) - 1) * cstride;
     redo &= redo - 1;
-    exact(c, *reinterpret_cast<const uint2*>(qr + 8 * c));
+    exact(c);
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (wpr > 1) {
@@ -404,9 +478,8 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
   const int gw = warp - grp * (T / 32), nw = T / 32;
   for (int i = threadIdx.x; i < 2 * kNbMaxGroups * kNbMaxWarps; i += blockDim.x) (&s_red[0][0][0])[i] = splat2(0.0f);
   const int chunks = (K + 7) / 8;
-  const bool vx = kFast || ((a.ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0);
-  const bool vdy = kFast || ((a.lddy % 8) == 0 && (reinterpret_cast<uintptr_t>(a.dy) & 15u) == 0);
-  const bool vdx = kFast || ((K % 8) == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 15u) == 0);
+  const uint16_t* const xend = a.x + static_cast<int64_t>(a.M - 1) * a.ldx + K;
+  const uint16_t* const yend = a.dy + static_cast<int64_t>(a.M - 1) * a.lddy + K;
   const float inv_k = __fdiv_rn(1.0f, static_cast<float>(K));
   const int64_t stride = static_cast<int64_t>(gridDim.x) * a.rg;
 
@@ -434,8 +507,8 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
         nx[j][0] = p.x; nx[j][1] = p.y; nx[j][2] = p.z; nx[j][3] = p.w;
         ny[j][0] = q.x; ny[j][1] = q.y; ny[j][2] = q.z; ny[j][3] = q.w;
       } else if (c < chunks) {
-        load8_raw(px - 8 * t, 8 * c, K, vx, nx[j]);
-        load8_raw(py - 8 * t, 8 * c, K, vdy, ny[j]);
+        load8_any(px - 8 * t, 8 * c, K, a.x, xend, nx[j]);
+        load8_any(py - 8 * t, 8 * c, K, a.dy, yend, ny[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) nx[j][i] = ny[j][i] = 0u;
@@ -532,7 +605,7 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
       if (kFast) {
         if (j < G - 1 || c < chunks) *reinterpret_cast<uint4*>(pd + 8 * j * T) = make_uint4(o[0], o[1], o[2], o[3]);
       } else if (c < chunks) {
-        store8_bf16(pd - 8 * t, 8 * c, K, vdx, o);
+        store8_bf16_any(pd - 8 * t, 8 * c, K, o);
       }
     }
     pd += sd;
@@ -692,42 +765,70 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const int8_t* __restri
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / lanes) + r;
   if (row >= M) return;
   const float s = __fdiv_rn(gamma[row], kQb);
-  const bool qv = (ldq % 16) == 0 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
+  const int8_t* const end = q + static_cast<int64_t>(M - 1) * ldq + K;
   const bool yv = (ldy % 8) == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
   for (int k0 = 16 * t; k0 < K; k0 += 16 * lanes) {
     uint32_t w[4], o[8];
-    load16_codes(q + row * ldq, k0, K, qv, w);
+    load16_codes_any(q + row * ldq, k0, K, q, end, w);
     dequant16(make_uint4(w[0], w[1], w[2], w[3]), s, o);
     store8_bf16(y + row * ldy, k0, K, yv, o);
     store8_bf16(y + row * ldy, k0 + 8, K, yv, o + 4);
   }
 }
 
-// The element-wise kernels for contiguous rows of a multiple of 16 columns (cpr
-// chunks of 16 a row, `total` in all): chunks are dealt to threads regardless
-// of the rows, and each thread's loads go out together.  The kernels above and
-// below wait for one chunk before they ask for the next (latency took three
-// quarters of their time: 7.8 us for 2048 x 2560 restored values, 22.9 for the
-// gate's gradients at 2048 x 6912).
+// The element-wise kernels for contiguous matrices of at least 16 columns (the
+// matrix as one row of `count` elements): chunks of 16 are dealt to threads
+// regardless of the rows, of which a chunk meets at most two, and each thread's
+// loads go out together.  The kernels above and below, for rows that are apart,
+// wait for one chunk before they ask for the next (latency took three quarters
+// of their time: 7.8 us for 2048 x 2560 restored values, 22.9 for the gate's
+// gradients at 2048 x 6912).  What is left of the last chunk goes element by
+// element.
+struct FlatChunk {
+  uint32_t row;   // of its first element
+  uint32_t left;  // elements of the chunk in that row
+};
+__device__ __forceinline__ FlatChunk flat_chunk(uint32_t i, uint32_t K) {
+  const uint32_t row = 16u * i / K;
+  return {row, K - (16u * i - row * K)};
+}
 constexpr int kFlatChunks = 4;
-__global__ void __launch_bounds__(256) dequant_flat_kernel(const uint4* __restrict__ q, const float* __restrict__ gamma,
-                                                           uint32_t cpr, uint32_t total, uint16_t* __restrict__ y) {
+__global__ void __launch_bounds__(256) dequant_flat_kernel(const int8_t* __restrict__ q, const float* __restrict__ gamma,
+                                                           uint32_t K, uint32_t count, uint16_t* __restrict__ y) {
   pdl_wait_primary();
   pdl_launch_dependents();
+  const uint32_t total = count / 16;
   const uint32_t i0 = blockIdx.x * (256 * kFlatChunks) + threadIdx.x;
   uint4 w[kFlatChunks];
-  float s[kFlatChunks];
+  float s[kFlatChunks], s1[kFlatChunks];
+  uint32_t left[kFlatChunks];
 #pragma unroll
   for (int j = 0; j < kFlatChunks; ++j) {
     const uint32_t i = min(i0 + 256 * j, total - 1);
-    w[j] = q[i];
-    s[j] = gamma[i / cpr];
+    w[j] = reinterpret_cast<const uint4*>(q)[i];
+    const FlatChunk f = flat_chunk(i, K);
+    left[j] = f.left;
+    s[j] = gamma[f.row];
+    s1[j] = f.left < 16 ? gamma[f.row + 1] : 0.0f;
   }
 #pragma unroll
   for (int j = 0; j < kFlatChunks; ++j) {
+    if (i0 + 256 * j >= total) continue;
     uint32_t o[8];
     dequant16(w[j], __fdiv_rn(s[j], kQb), o);
-    if (i0 + 256 * j < total) st_global_v8(y + 16 * static_cast<size_t>(i0 + 256 * j), o);
+    if (left[j] < 16) {  // the next row's part
+      uint32_t n[8];
+      dequant16(w[j], __fdiv_rn(s1[j], kQb), n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[e] = 2 * e >= left[j] ? n[e] : 2 * e + 1 >= left[j] ? (o[e] & 0xFFFFu) | (n[e] & 0xFFFF0000u) : o[e];
+    }
+    st_global_v8(y + 16 * static_cast<size_t>(i0 + 256 * j), o);
+  }
+  if (blockIdx.x == 0 && threadIdx.x < count % 16) {
+    const uint32_t e = 16 * total + threadIdx.x;
+    y[e] = static_cast<uint16_t>(
+        pack_bf16x2(__fmul_rn(static_cast<float>(q[e]), __fdiv_rn(gamma[e / K], kQb)), 0.0f));
   }
 }
 
@@ -748,7 +849,7 @@ struct GluSaveArgs {
 
 // Warps and chunks as in layernorm_kernel; h is cheaper computed again (three
 // bf16x2 operations a pair) than kept.
-template <int G>
+template <bool kAny, int G>
 __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
     relu2_glu_quant_kernel(const GluSaveArgs a) {
   constexpr bool kRegs = G > 0;
@@ -764,18 +865,18 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
   const bool active = row < a.M;
   const uint16_t* gr = a.g + (active ? row : 0) * a.ldg;
   const uint16_t* ur = a.u + (active ? row : 0) * a.ldu;
-  const bool vg = kRegs || ((a.ldg % 8) == 0 && (reinterpret_cast<uintptr_t>(a.g) & 15u) == 0);
-  const bool vu = kRegs || ((a.ldu % 8) == 0 && (reinterpret_cast<uintptr_t>(a.u) & 15u) == 0);
+  const uint16_t* const gend = a.g + static_cast<int64_t>(a.M - 1) * a.ldg + N;
+  const uint16_t* const uend = a.u + static_cast<int64_t>(a.M - 1) * a.ldu + N;
   const int chunks = (N + 7) / 8, cstride = 32 * wpr, c0 = sub * 32 + lane;
 
   auto load = [&](int c, uint32_t (&r)[2][4]) {
-    if (kRegs) {
+    if (!kAny) {
       const uint4 t = *reinterpret_cast<const uint4*>(gr + 8 * c), y = *reinterpret_cast<const uint4*>(ur + 8 * c);
       r[0][0] = t.x; r[0][1] = t.y; r[0][2] = t.z; r[0][3] = t.w;
       r[1][0] = y.x; r[1][1] = y.y; r[1][2] = y.z; r[1][3] = y.w;
     } else {
-      load8_raw(gr, 8 * c, N, vg, r[0]);
-      load8_raw(ur, 8 * c, N, vu, r[1]);
+      load8_any(gr, 8 * c, N, a.g, gend, r[0]);
+      load8_any(ur, 8 * c, N, a.u, uend, r[1]);
     }
   };
   uint32_t v[GR][2][4];  // g, u
@@ -834,7 +935,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
   int32_t sum = 0;
   uint32_t redo = 0u;  // chunks with codes that take the exact quotient
   const size_t at = static_cast<size_t>(active ? row : 0) * N;
-  const bool vq = kRegs || ((N % 8) == 0 && ((reinterpret_cast<uintptr_t>(a.qg) | reinterpret_cast<uintptr_t>(a.qu) |
+  const bool vq = !kAny || ((N % 8) == 0 && ((reinterpret_cast<uintptr_t>(a.qg) | reinterpret_cast<uintptr_t>(a.qu) |
                                               reinterpret_cast<uintptr_t>(a.qh)) & 7u) == 0);
   int8_t* const out[3] = {a.qg + at, a.qu + at, a.qh + at};
   auto values = [&](int p, const uint32_t (&r)[2][4], float2 (&f)[4]) {
@@ -895,41 +996,56 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
 }
 
 // Two of dg = RNb(2 dh r u~) and du = RNb(dh r^2), r = max(g~, 0), of two codes' values g, u each.
-__device__ __forceinline__ void glu_grads2(float2 g, float2 u, uint32_t dh, float sg, float su, uint32_t& dg,
+__device__ __forceinline__ void glu_grads2(float2 g, float2 u, uint32_t dh, float2 sg, float2 su, uint32_t& dg,
                                            uint32_t& du) {
   const float2 d = bf16_2(dh);
-  float2 rp = __fmul2_rn(g, splat2(sg));
+  float2 rp = __fmul2_rn(g, sg);
   rp = make_float2(fmaxf(rp.x, 0.0f), fmaxf(rp.y, 0.0f));
   const float2 dr = __fmul2_rn(d, rp);
-  const float2 p = __fmul2_rn(__fadd2_rn(dr, dr), __fmul2_rn(u, splat2(su))), q = __fmul2_rn(dr, rp);
+  const float2 p = __fmul2_rn(__fadd2_rn(dr, dr), __fmul2_rn(u, su)), q = __fmul2_rn(dr, rp);
   dg = pack_bf16x2(p.x, p.y);
   du = pack_bf16x2(q.x, q.y);
 }
 
-// As dequant_flat_kernel, two chunks a thread (64 bytes each).
+// As dequant_flat_kernel, two chunks a thread (64 bytes each).  kSplit: chunks may meet two rows (rows of a multiple of
+// 16 columns: 11.7 us at 4096 x 2560, with the selects 15.2).
+template <bool kSplit>
 __global__ void __launch_bounds__(256, 4)
-    relu2_glu_backward_flat_kernel(const uint16_t* __restrict__ dh, const uint4* __restrict__ qg,
-                                   const float* __restrict__ gg, const uint4* __restrict__ qu,
-                                   const float* __restrict__ gu, uint32_t cpr, uint32_t total,
+    relu2_glu_backward_flat_kernel(const uint16_t* __restrict__ dh, const int8_t* __restrict__ qg,
+                                   const float* __restrict__ gg, const int8_t* __restrict__ qu,
+                                   const float* __restrict__ gu, uint32_t N, uint32_t count,
                                    uint16_t* __restrict__ dg, uint16_t* __restrict__ du) {
   pdl_wait_primary();
   pdl_launch_dependents();
+  const uint32_t total = count / 16;
   const uint32_t i0 = blockIdx.x * 512 + threadIdx.x;
   uint4 wg[2], wu[2];
-  uint32_t h[2][8];
-  float sg[2], su[2];
+  uint32_t h[2][8], left[2];
+  float sg[2][2], su[2][2];  // of the chunk's row and the next
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const uint32_t i = min(i0 + 256 * j, total - 1);
-    wg[j] = qg[i];
-    wu[j] = qu[i];
+    wg[j] = reinterpret_cast<const uint4*>(qg)[i];
+    wu[j] = reinterpret_cast<const uint4*>(qu)[i];
     ld_global_nc_v8(dh + 16 * static_cast<size_t>(i), h[j]);
-    sg[j] = gg[i / cpr];
-    su[j] = gu[i / cpr];
+    const FlatChunk f = flat_chunk(i, N);
+    left[j] = f.left;
+    sg[j][0] = gg[f.row];
+    su[j][0] = gu[f.row];
+    if (kSplit) {
+      const uint32_t next = f.row + (f.left < 16 ? 1u : 0u);
+      sg[j][1] = gg[next];
+      su[j][1] = gu[next];
+    }
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const float a = __fdiv_rn(sg[j], kQb), b = __fdiv_rn(su[j], kQb);
+    float a[2], b[2];
+#pragma unroll
+    for (int r = 0; r < (kSplit ? 2 : 1); ++r) {
+      a[r] = __fdiv_rn(sg[j][r], kQb);
+      b[r] = __fdiv_rn(su[j][r], kQb);
+    }
     const uint32_t g4[4] = {wg[j].x, wg[j].y, wg[j].z, wg[j].w}, u4[4] = {wu[j].x, wu[j].y, wu[j].z, wu[j].w};
     uint32_t og[8], ou[8];
 #pragma unroll
@@ -938,13 +1054,26 @@ __global__ void __launch_bounds__(256, 4)
       codes4_f32(g4[i], fg);
       codes4_f32(u4[i], fu);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) glu_grads2(fg[e], fu[e], h[j][2 * i + e], a, b, og[2 * i + e], ou[2 * i + e]);
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t k = 4 * i + 2 * e;
+        const float2 sa = make_float2(kSplit && k >= left[j] ? a[1] : a[0], kSplit && k + 1 >= left[j] ? a[1] : a[0]);
+        const float2 sb = make_float2(kSplit && k >= left[j] ? b[1] : b[0], kSplit && k + 1 >= left[j] ? b[1] : b[0]);
+        glu_grads2(fg[e], fu[e], h[j][2 * i + e], sa, sb, og[2 * i + e], ou[2 * i + e]);
+      }
     }
     if (i0 + 256 * j < total) {
       const size_t at = 16 * static_cast<size_t>(i0 + 256 * j);
       st_global_v8(dg + at, og);
       st_global_v8(du + at, ou);
     }
+  }
+  if (blockIdx.x == 0 && threadIdx.x < count % 16) {
+    const uint32_t e = 16 * total + threadIdx.x, row = e / N;
+    uint32_t p, q;
+    glu_grads2(splat2(static_cast<float>(qg[e])), splat2(static_cast<float>(qu[e])), dh[e],
+               splat2(__fdiv_rn(gg[row], kQb)), splat2(__fdiv_rn(gu[row], kQb)), p, q);
+    dg[e] = static_cast<uint16_t>(p);
+    du[e] = static_cast<uint16_t>(q);
   }
 }
 
@@ -960,17 +1089,17 @@ __global__ void __launch_bounds__(256) relu2_glu_backward_kernel(
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / lanes) + r;
   if (row >= M) return;
   const float sg = __fdiv_rn(gg[row], kQb), su = __fdiv_rn(gu[row], kQb);
-  const bool vq = (N % 16) == 0 && ((reinterpret_cast<uintptr_t>(qg) | reinterpret_cast<uintptr_t>(qu)) & 15u) == 0;
-  const bool vh = (lddh % 8) == 0 && (reinterpret_cast<uintptr_t>(dh) & 15u) == 0;
+  const uint16_t* const end = dh + static_cast<int64_t>(M - 1) * lddh + N;
+  const size_t codes = static_cast<size_t>(M) * N;
   const bool vo = (N % 8) == 0 && ((reinterpret_cast<uintptr_t>(dg) | reinterpret_cast<uintptr_t>(du)) & 15u) == 0;
   const uint16_t* dhr = dh + row * lddh;
   const size_t at = static_cast<size_t>(row) * N;
   for (int k0 = 16 * t; k0 < N; k0 += 16 * lanes) {
     uint32_t wg[4], wu[4], h0[4], h1[4];
-    load16_codes(qg + at, k0, N, vq, wg);
-    load16_codes(qu + at, k0, N, vq, wu);
-    load8_raw(dhr, k0, N, vh, h0);
-    load8_raw(dhr, k0 + 8, N, vh, h1);
+    load16_codes_any(qg + at, k0, N, qg, qg + codes, wg);
+    load16_codes_any(qu + at, k0, N, qu, qu + codes, wu);
+    load8_any(dhr, k0, N, dh, end, h0);
+    load8_any(dhr, k0 + 8, N, dh, end, h1);
     uint32_t og[8], ou[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -979,7 +1108,7 @@ __global__ void __launch_bounds__(256) relu2_glu_backward_kernel(
       codes4_f32(wu[i], fu);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        glu_grads2(fg[h], fu[h], i < 2 ? h0[2 * i + h] : h1[2 * (i - 2) + h], sg, su, og[2 * i + h], ou[2 * i + h]);
+        glu_grads2(fg[h], fu[h], i < 2 ? h0[2 * i + h] : h1[2 * (i - 2) + h], splat2(sg), splat2(su), og[2 * i + h], ou[2 * i + h]);
     }
     store8_bf16(dg + at, k0, N, vo, og);
     store8_bf16(dg + at, k0 + 8, N, vo, og + 4);

@@ -719,3 +719,41 @@ def test_product_nan_stays_in_its_row():
         dW2 = bl.backward_weight(bad, q, gamma)
         rows = [i for i in range(N) if i != 77]
         assert torch.equal(dW2[rows], dW[rows]) and bool(dW2[77].isnan().all())
+
+
+# ---------------------------------------------------------------- widths and strides of every alignment
+@pytest.mark.parametrize("K", [17, 31, 250, 2561, 2562, 2564, 5003, 12299])
+@pytest.mark.parametrize("M", [1, 2, 150])
+def test_every_alignment(M, K):
+    """Rows that start anywhere in a 16-byte block, the first and the last of a buffer among them."""
+    w, b = torch.rand(K, device=DEV) + 0.5, torch.rand(K, device=DEV)
+    x, dy = _rand(M + K, M, K, outliers=True), _rand(M * K, M, K, scale=1e-3)
+    mean, rstd = _moments(x, 1e-5)
+    y, m1, r1 = bl.layernorm(x, w, b, 1e-5, want_stats=True)
+    assert torch.equal(m1, mean) and torch.equal(r1, rstd) and torch.equal(y, _normed(x, w, b, mean, rstd).to(BF))
+    q, gamma, rs = bl.layernorm_quant_act(x, w, b, 1e-5)
+    q0, g0, rs0 = _codes(_normed(x, w, b, mean, rstd))
+    assert torch.equal(q, q0) and torch.equal(gamma, g0) and torch.equal(rs, rs0)
+    assert torch.equal(bl.dequant_act(q, gamma), _values(q, gamma).to(BF))
+    dx, dw, db = bl.layernorm_backward(dy, x, w, mean, rstd)
+    dx0, dw0, db0, size, dws, dbs = _norm_backward_ref(dy, x, w, mean, rstd, K)
+    _close(dx, dx0, HALF * dx0.abs() * (1 + HALF) + 128 * U * size, "dx")
+    _close(dw, dw0, (M + 200) * U * dws, "dw")
+    c = bl.relu2_glu_quant_act(x, dy)
+    for v, qq, gg in ((x, c.q_g, c.gamma_g), (dy, c.q_u, c.gamma_u), (_glu_h(x, dy), c.q_h, c.gamma_h)):
+        q0, g0, _ = _codes(v.float())
+        assert torch.equal(gg, g0) and torch.equal(qq, q0)
+    dg, du = bl.relu2_glu_backward(dy, *c[:4])
+    for off in range(1, 9, 3):  # the same values elsewhere in memory, rows apart and not
+        for pad in (0, 5, 8):
+            xs, ds = _strided(x, pad, off), _strided(dy, pad + 3, off)
+            assert torch.equal(bl.layernorm(xs, w, b, 1e-5), y)
+            for got, want in zip(bl.layernorm_quant_act(xs, w, b, 1e-5), (q, gamma, rs)):
+                assert torch.equal(got, want)
+            for got, want in zip(bl.layernorm_backward(ds, xs, w, mean, rstd), (dx, dw, db)):
+                assert torch.equal(got, want)
+            for got, want in zip(bl.relu2_glu_quant_act(xs, ds), c):
+                assert torch.equal(got, want)
+            for got, want in zip(bl.relu2_glu_backward(ds, *c[:4]), (dg, du)):
+                assert torch.equal(got, want)
+            assert torch.equal(bl.dequant_act(_strided(c.q_h, pad, off), c.gamma_h), bl.dequant_act(c.q_h, c.gamma_h))
