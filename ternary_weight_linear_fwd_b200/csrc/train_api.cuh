@@ -277,15 +277,34 @@ size_t bi_b_bytes(const GgPlan& p, int N, int K, int nm_m) {
   return bi_dense(p, N, K) ? static_cast<size_t>(N) * k16(K) * 2 : nm_m ? static_cast<size_t>(N) * dense_ld(K) : 0;
 }
 
-// Puts dy's rows where TMA can step them, if they are not.
-bitlinear_status gg_dy(const uint16_t** dy, int64_t lddy, int M, int N, uint8_t* ws, const GgLayout& l,
-                       cudaStream_t s, int sm_count) {
-  if (l.lddy == lddy) return BITLINEAR_OK;
-  uint16_t* d = reinterpret_cast<uint16_t*>(ws + l.dy);
-  const bitlinear_status st = launch(pad_rows_kernel<uint16_t>, dim3(std::min(M, 16 * sm_count)), dim3(256), 0, s, false,
-                                     *dy, lddy, static_cast<int64_t>(M), N, d, l.lddy);
-  *dy = d;
-  return st;
+// Puts the rows of dy (l.lddy is another stride) and of the codes (q_out) where TMA can step them, if they are not.
+bitlinear_status gg_pad(const uint16_t** dy, int64_t lddy, const int8_t* q, int64_t ldq, int8_t* q_out, int M, int N,
+                        int K, uint8_t* ws, const GgLayout& l, cudaStream_t s) {
+  const bool pad = l.lddy != lddy;
+  if (!pad && !q_out) return BITLINEAR_OK;
+  PadArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  auto blocks = [&](int64_t chunks) { return static_cast<unsigned>((static_cast<int64_t>(M) * chunks + 255) / 256); };
+  unsigned grid = 0;
+  if (pad) {
+    a.dy = *dy;
+    a.lddy = lddy;
+    a.ldd = l.lddy;
+    a.dy_out = reinterpret_cast<uint16_t*>(ws + l.dy);
+    *dy = a.dy_out;
+    grid = a.dy_blocks = blocks(l.lddy / 8);
+  }
+  if (q_out) {
+    a.q = q;
+    a.ldq = ldq;
+    a.ldqd = k16(K);
+    a.q_out = q_out;
+    grid += blocks(k16(K) / 16);
+  }
+  return launch(pad_rows_kernel, dim3(grid), dim3(256), 0, s, false, a);
 }
 
 template <bool kWeight>
@@ -579,19 +598,16 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
   const GgLayout l = gg_layout(p, M, N, lddy, bw_b_bytes(p, M, K, ldq));
   if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);
-  if (st != BITLINEAR_OK) return st;
   const bool dense = bw_dense(p, M, K);
-  if (dense) {
+  int8_t* const padded = !dense && ldq % 16 ? reinterpret_cast<int8_t*>(ws + l.b) : nullptr;
+  st = gg_pad(&dy, lddy, q, ldq, padded, M, N, K, ws, l, s);
+  if (st == BITLINEAR_OK && dense)
     st = dequant_launch(q, ldq, gamma, M, K, reinterpret_cast<uint16_t*>(ws + l.b), k16(K), s, true, dev->sm_count);
-  } else if (ldq % 16) {
-    int8_t* d = reinterpret_cast<int8_t*>(ws + l.b);
-    st = launch(pad_rows_kernel<int8_t>, dim3(std::min(M, 16 * dev->sm_count)), dim3(256), 0, s, true, q, ldq,
-                static_cast<int64_t>(M), K, d, k16(K));
-    q = d;
+  if (st != BITLINEAR_OK) return st;
+  if (padded) {
+    q = padded;
     ldq = k16(K);
   }
-  if (st != BITLINEAR_OK) return st;
   CUtensorMap mA, mB;
   if (!make_map_u8(&mA, dy, 2 * static_cast<uint64_t>(N), M, 2 * static_cast<uint64_t>(l.lddy), 128, kGgRed, 128) ||
       !(dense ? make_map_u8(&mB, ws + l.b, 2 * static_cast<uint64_t>(K), M, 2 * static_cast<uint64_t>(k16(K)), 128,
@@ -664,7 +680,7 @@ bitlinear_status bitlinear_backward_input(const bitlinear_weights* w, const uint
   const GgPlan p = gg_plan(M, K, N, 0.43, dev->sm_count);
   const GgLayout l = gg_layout(p, M, N, lddy, bi_b_bytes(p, N, K, w->nm_m));
   if (l.total > 0 && (!workspace || !aligned32(workspace) || workspace_bytes < l.total)) return BITLINEAR_ERR_WORKSPACE;
-  st = gg_dy(&dy, lddy, M, N, ws, l, s, dev->sm_count);
+  st = gg_pad(&dy, lddy, nullptr, 0, nullptr, M, N, K, ws, l, s);
   if (st != BITLINEAR_OK) return st;
   const uint8_t* codes = w->codes;
   const bool dense = bi_dense(p, N, K);

@@ -611,14 +611,36 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
 }
 
 // ----------------------------------------------------------------- operands put in order
-// Rows whose stride TMA cannot step (not a multiple of 16 bytes), copied to rows that it can; T: 2-byte or 1-byte.
-template <typename T>
-__global__ void __launch_bounds__(256) pad_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t rows, int cols,
-                                                       T* __restrict__ dst, int64_t ldd) {
+// Rows whose stride TMA cannot step (not a multiple of 16 bytes), copied to rows that it can, zero behind their ends:
+// of dy, of the codes, or of both in one launch (the first dy_blocks CTAs take dy, 8 values a thread; the others the
+// codes, 16 a thread).
+struct PadArgs {
+  const uint16_t* dy;
+  int64_t lddy, ldd;      // of the source, of the copy
+  uint16_t* dy_out;
+  const int8_t* q;
+  int64_t ldq, ldqd;
+  int8_t* q_out;
+  int M, N, K;
+  unsigned dy_blocks;     // 0: dy is not copied
+};
+__global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < cols; c += 256) dst[r * ldd + c] = src[r * ld + c];
+  const bool dy = blockIdx.x < a.dy_blocks;
+  const unsigned per = static_cast<unsigned>(dy ? a.ldd / 8 : a.ldqd / 16);  // chunks of a row
+  const int64_t at = static_cast<int64_t>(dy ? blockIdx.x : blockIdx.x - a.dy_blocks) * 256 + threadIdx.x;
+  const int64_t row = at / per;
+  const int c = static_cast<int>(at - row * per);
+  if (row >= a.M) return;
+  uint32_t w[4];
+  if (dy) {
+    load8_any(a.dy + row * a.lddy, 8 * c, a.N, a.dy, a.dy + (a.M - 1) * a.lddy + a.N, w);
+    *reinterpret_cast<uint4*>(a.dy_out + row * a.ldd + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    load16_codes_any(a.q + row * a.ldq, 16 * c, a.K, a.q, a.q + (a.M - 1) * a.ldq + a.K, w);
+    *reinterpret_cast<uint4*>(a.q_out + row * a.ldqd + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // N:M rows expanded to dense codes (16 weights a thread), the layout of the
