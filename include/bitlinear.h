@@ -409,17 +409,18 @@ bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w, const uin
  *
  * Rows may be strided: ld* counts elements between rows and is at least the
  * row's length.  Matrices whose ld is a multiple of 8 (bf16) or 16 (codes) and
- * whose address is 16-byte aligned are read 16 bytes at a time; the two
- * gradient products refuse (ALIGN) such an ld with another address, and copy
- * the rows of any other ld into their workspace first.  Outputs are contiguous,
+ * whose address is 16-byte aligned are read fastest; the two gradient products
+ * refuse (ALIGN) such an ld with another address, and copy the rows of any other
+ * ld into their workspace first (bitlinear_backward_input only for more than a
+ * few tokens).  Outputs are contiguous,
  * are written whole and may not overlap inputs.  Same inputs give the same
  * bits: no sum depends on the order in which CTAs finish.
  * ------------------------------------------------------------------------- */
 #define BITLINEAR_FLAG_ACCUMULATE 0x40u /* bitlinear_backward_weight: add to dW instead of writing it */
 
 /* Layer norm.  Per row: s1 = sum x, s2 = sum x^2 in fp64; mean = RN32(s1 / K);
- * var = RN32(max(0, (s2 - s1^2 / K) / K)); rstd = RN32(1 / sqrt(var + eps)) (root
- * and quotient in fp64); xn = RN32(RN32(RN32(x - mean) * rstd) * w), then
+ * var = RN32(max(0, (s2 - s1^2 / K) / K)); rstd = RN32(1 / sqrt(var + eps)) (all in
+ * fp64 before their one rounding); xn = RN32(RN32(RN32(x - mean) * rstd) * w), then
  * RN32(xn + b) with a bias; y = bf16 of xn.
  * x        device, bf16 bits [M, ldx];  w, b  device, fp32 [K] (b may be NULL).
  * eps      0 <= eps <= 1 (with eps = 0 a constant row is undefined).
@@ -431,7 +432,8 @@ bitlinear_status bitlinear_layernorm(const uint16_t* x, int64_t ldx, int32_t M, 
 
 /* The same xn, quantised per token as bitlinear_quant_act does (xn is not
  * rounded to bf16 first): what a BitLinear behind a layer norm reads, and at
- * once the 8-bit checkpoint of its input.  q int8 [M, K], gamma fp32 [M],
+ * once the 8-bit checkpoint of its input.  A row with a NaN or an infinity gets
+ * gamma = NaN (and codes without meaning).  q int8 [M, K], gamma fp32 [M],
  * rowsum int32 [M] (may be NULL).  Errors: as bitlinear_layernorm. */
 bitlinear_status bitlinear_layernorm_quant_act(const uint16_t* x, int64_t ldx, int32_t M, int32_t K, const float* w,
                                                const float* b, float eps, int8_t* q, float* gamma, int32_t* rowsum,
@@ -490,7 +492,9 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
 
 /* dW = dy^T x~: the gradient of a BitLinear's latent weights from the 8-bit
  * checkpoint of its input, x~ restored in bf16 (bitlinear_dequant_act), the
- * products exact and the sums in fp32.  For N:M weights this is the gradient
+ * products exact and the sums in fp32 (pieces of at most 896 tokens on the tensor
+ * cores, which cut off below the last place, then rounded additions: together
+ * within about 1e-6 of the sum of the terms' magnitudes).  For N:M weights this is the gradient
  * of every latent weight, kept or not (the "dual" estimator of the
  * Sparse-BitNet review, section 3.3).
  * dy       device, bf16 bits [M, lddy] (N used);  q  device, int8 [M, ldq] (K
