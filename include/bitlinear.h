@@ -512,7 +512,9 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
                                            void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
 
 /* dx = alpha dy W_t (+ add): the gradient of a BitLinear's input, the products
- * exact, the sums in fp32, one rounding to bf16 at the end.  add is the
+ * exact, the sums in fp32 (on the tensor cores, which cut off below the last
+ * place: about 1e-9 of the sum a term, less than the rounding to bf16 up to N =
+ * 2^20), one rounding to bf16 at the end.  add is the
  * gradient that reaches the same input another way (the up projection's beside
  * the gate's, or the residual path's).
  * w        dense or N:M weights.
