@@ -46,6 +46,7 @@
 // of the workspace, and grad_reduce_kernel adds the parts in order and
 // finishes the tile: no atomics, the same bits every time.
 #pragma once
+#include "nm_decode.cuh"
 #include "train_rows.cuh"
 
 namespace bl {
@@ -652,51 +653,6 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
 
 // N:M rows expanded to dense codes (16 weights a thread), the layout of the
 // dense matrix of the same size; positions past K hold code 1.
-struct ExpandArgs {
-  const uint8_t* codes;
-  const uint8_t* meta;
-  int64_t ldc, ldm, ldd;  // ldd: row stride of the dense codes, bytes (bf16: of the values, elements)
-  int N, K, nm_n, nm_m;
-  uint32_t* out;
-};
-
-// The 16 dense codes from k0 (a multiple of 16) of row n of an N:M matrix.  K is a multiple of m, so the 16 lie in
-// whole blocks; positions past K get code 1 (a row's bytes end with zeros, which name no kept position of 1:8 ..
-// 7:8 and are masked for 2:4).
-__device__ __forceinline__ uint32_t nm_codes16(const ExpandArgs& a, int64_t n, int k0) {
-  const int w = k0 >> 4;
-  const uint32_t mt = *reinterpret_cast<const uint16_t*>(a.meta + n * a.ldm + 2 * w);  // 4 nibbles, or 2 masks
-  uint32_t o = 0x55555555u;
-  if (a.nm_m == 4) {
-    const uint32_t c = *reinterpret_cast<const uint16_t*>(a.codes + n * a.ldc + 2 * w);  // 8 kept codes
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint32_t s0 = 8 * b + 2 * ((mt >> (4 * b)) & 3u), s1 = 8 * b + 2 * ((mt >> (4 * b + 2)) & 3u);
-      // code 1 (01) is there: its place becomes c by flipping c ^ 1
-      if (k0 + 4 * b < a.K) o ^= ((((c >> (4 * b)) & 3u) ^ 1u) << s0) ^ ((((c >> (4 * b + 2)) & 3u) ^ 1u) << s1);
-    }
-  } else {
-    const int bits = 4 * a.nm_n;  // kept codes of two blocks
-    const uint8_t* p = a.codes + n * a.ldc + ((w * bits) >> 3);
-    const int shift = (w * bits) & 7;
-    uint64_t v = 0;
-    for (int i = 0; 8 * i < bits + shift; ++i) v |= static_cast<uint64_t>(p[i]) << (8 * i);
-    uint32_t c = static_cast<uint32_t>(v >> shift);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t kept = c >> (2 * a.nm_n * b);
-      if (k0 + 8 * b < a.K)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if ((mt >> (8 * b + j)) & 1u) {
-            o ^= ((kept & 3u) ^ 1u) << (16 * b + 2 * j);
-            kept >>= 2;
-          }
-    }
-  }
-  return o;
-}
-
 __global__ void __launch_bounds__(256) nm_expand_kernel(const ExpandArgs a) {
   pdl_wait_primary();
   pdl_launch_dependents();
