@@ -458,6 +458,8 @@ bitlinear_status bitlinear_layernorm_backward(const uint16_t* dy, int64_t lddy, 
  * bitlinear_forward_norm: with r = 1 / sqrt(mean_k(x^2) + eps) (recomputed),
  * xh = x r and a = dy g
  *   dx = r (a - xh mean_k(a xh)),  dg = sum_m dy xh.
+ * Sums in fp32, and in fp64 for rows whose mean square leaves 2^-100 .. 2^100,
+ * so every row of finite entries has the formula's gradient (r itself is fp32).
  * Arguments and errors as bitlinear_layernorm_backward; eps as in the forward. */
 bitlinear_status bitlinear_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                                             int32_t M, int32_t K, const float* g, float eps, uint16_t* dx, float* dg,

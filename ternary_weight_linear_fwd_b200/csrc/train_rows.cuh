@@ -483,6 +483,34 @@ constexpr int kNbMaxGroups = 8;                                // one named barr
 constexpr int kNbMaxWarps = 24;                                // of a group
 constexpr int kNbMaxK = 8 * 4 * nb_max_threads(4);             // longer rows take the split kernels
 
+// RMSNorm of a row whose squares fp32 cannot add up (mean square beyond 2^100 or, with next to no eps, below 2^-100): r
+// and mean_k(a xh) with sums in fp64, which hold the square of every bf16 value.  Called by whole warps, each of which
+// reads the row again by itself.
+constexpr uint32_t kRmsLow = 0x0D800000u, kRmsHigh = 0x71800000u;  // bits of 2^-100 and 2^100
+constexpr uint32_t kRmsMark = 0xFFFFFFFFu;  // two bf16 that no conversion gives: its NaN is 0x7FFF
+__device__ __forceinline__ bool rms_far(float m) { return __float_as_uint(m) - kRmsLow > kRmsHigh - kRmsLow; }
+__device__ __forceinline__ float rsqrt_normal(float v) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __noinline__ float2 rms_far_row(const uint16_t* x, const uint16_t* dy, const float* w, int K, float eps) {
+  const int lane = threadIdx.x & 31;
+  auto sum = [](double v) {
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  double ss = 0.0, c = 0.0;
+  for (int k = lane; k < K; k += 32) {
+    const double v = bf16_bits_to_f32(x[k]);
+    ss = __fma_rn(v, v, ss);
+  }
+  const double r = 1.0 / sqrt(sum(ss) / K + static_cast<double>(eps));
+  for (int k = lane; k < K; k += 32)
+    c = __fma_rn(static_cast<double>(bf16_bits_to_f32(dy[k])) * w[k], bf16_bits_to_f32(x[k]) * r, c);
+  return make_float2(__double2float_rn(r), __double2float_rn(sum(c) / K));
+}
+
 // kFast: 16-byte accesses everywhere (columns past K, a whole chunk then, are read from the last chunk and zeroed).
 template <bool kLayer, bool kFast, int G>
 __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(const NbArgs a) {
@@ -513,6 +541,7 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
     for (int i = 0; i < 4; ++i) dwv[j][i] = dbv[j][i] = splat2(0.0f);
   uint32_t nx[G][4], ny[G][4];  // the next row's words
   float nmean = 0.0f, nrstd = 1.0f;
+  bool far = false;  // RMSNorm: some row was put off (rms_far); it adds nothing here and is marked in dx
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.rg + grp;
   // the thread's first chunk of the row to load next and of the row to write, and the steps between a group's rows
   const uint16_t* px = a.x + row * a.ldx + 8 * t;
@@ -605,9 +634,13 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
     }
     c1 *= inv_k;
     c2 *= inv_k;
+    bool out = false;
     if (!kLayer) {
-      rstd = rsqrtf(c1 + a.eps);  // within 2 ulp, as good as the sums
-      c2 *= rstd * rstd;          // against x instead of xh
+      const float m = c1 + a.eps;
+      out = rms_far(m);
+      rstd = out ? 0.0f : rsqrt_normal(m);  // within 2 ulp, as good as the sums
+      c2 *= rstd * rstd;                    // against x instead of xh
+      far |= out;
     }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -625,6 +658,7 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
         if (kLayer) dbv[j][i] = __fadd2_rn(dbv[j][i], yf[j][i]);
         o[i] = pack_bf16x2(s.x, s.y);
       }
+      if (j == 0 && out) o[0] = kRmsMark;
       if (kFast) {
         if (j < G - 1 || c < chunks) *reinterpret_cast<uint4*>(pd + 8 * j * T) = make_uint4(o[0], o[1], o[2], o[3]);
       } else if (c < chunks) {
@@ -632,6 +666,31 @@ __global__ void __launch_bounds__(nb_max_threads(G), 1) norm_backward_kernel(con
       }
     }
     pd += sd;
+  }
+  if (!kLayer && far) {  // the same for the whole group
+    // the rows put off, known by their first entry; here, since the same branch inside the rows above costs them time
+    // even where none takes it (4096 x 2560: 15.4 us, so 14.7, without any such rows 14.3; 8192 x 640: 13.1, 11.5, 11.5)
+    bar_sync_n(1 + grp, T);
+#pragma unroll 1
+    for (row = static_cast<int64_t>(blockIdx.x) * a.rg + grp; row < a.M; row += stride) {
+      const uint16_t *xr = a.x + row * a.ldx, *yr = a.dy + row * a.lddy;
+      uint16_t* const dr = a.dx + row * K;
+      if (*dr != static_cast<uint16_t>(kRmsMark)) continue;
+      bar_sync_n(1 + grp, T);  // every warp has read the mark
+      const float2 v = rms_far_row(xr, yr, a.w, K, a.eps);
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = 8 * (t + j * T) + e;
+          if (k < K) {
+            const float xh = bf16_bits_to_f32(xr[k]) * v.x, dy = bf16_bits_to_f32(yr[k]);
+            dr[k] = static_cast<uint16_t>(pack_bf16x2(fmaf(xh, -v.y, dy * a.w[k]) * v.x, 0.0f));
+            float& sum = (e & 1) ? dwv[j][e >> 1].y : dwv[j][e >> 1].x;
+            sum = fmaf(dy, xh, sum);
+          }
+        }
+    }
   }
   pdl_launch_dependents();
   // the groups' column sums, added in order of the groups; the last writes the CTA's partial row
@@ -703,8 +762,14 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NbArgs a
   c1 = __fdiv_rn(c1, static_cast<float>(K));
   c2 = __fdiv_rn(c2, static_cast<float>(K));
   if (!kLayer) {
-    rstd = __fdiv_rn(1.0f, __fsqrt_rn(c1 + a.eps));
-    c2 *= rstd;
+    if (rms_far(c1 + a.eps)) {
+      const float2 far = rms_far_row(xr, dyr, a.w, K, a.eps);
+      rstd = far.x;
+      c2 = far.y;
+    } else {
+      rstd = __fdiv_rn(1.0f, __fsqrt_rn(c1 + a.eps));
+      c2 *= rstd;
+    }
     if (threadIdx.x == 0) rstd_out[row] = rstd;
   }
   for (int k = threadIdx.x; k < K; k += 1024) {

@@ -1,0 +1,55 @@
+"""BitLinear's training side on the GPU where values leave the ordinary range, against plain forms in 64 bits.
+
+Tolerances are those of test_gpu_training.py, with what is added derived beside each check."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import ternary_weight_linear_fwd_b200 as bl  # noqa: E402
+from test_gpu_training import BF, DEV, HALF, U, _close, _gen, _norm_backward_ref, _rand, _strided  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from ternary_weight_linear_fwd_b200 import build as b
+    b.build()
+    yield
+    torch.cuda.synchronize()
+    assert bl.device_status() == 0
+
+
+# ---------------------------------------------------------------- RMSNorm: rows whose squares fp32 cannot add up
+@pytest.mark.parametrize("K", [9, 203, 2560, 6150, 11008, 12290, 16384])
+@pytest.mark.parametrize("eps", [1e-5, 0.0])
+def test_rmsnorm_backward_far_rows(K, eps):
+    """Rows of entries near 1e18 to 3e38, whose squares overflow, and, where no eps hides them, of entries near 1e-25 to
+    1e-37, whose squares vanish, among ordinary ones: each row's gradient is that of the formula."""
+    M = 40
+    x = torch.randn(M, K, device=DEV, generator=_gen(K)).clamp(-4, 4)
+    far = {1: 1e17, 4: 1e18, 7: 3e19, 20: 1e25, 21: 1e36, 39: 8e37}
+    if eps == 0.0:
+        far.update({2: 1e-18, 5: 1e-21, 11: 1e-25, 30: 1e-37})
+    for row, scale in far.items():
+        x[row] *= scale
+    x = x.to(BF)
+    assert bool(torch.isfinite(x.float()).all())
+    dy = _rand(K + 1, M, K, scale=1e-3)
+    g = 1 + 0.1 * torch.randn(K, device=DEV, generator=_gen(1))
+    dx, dg = bl.rmsnorm_backward(dy, x, g, eps)
+    r = 1.0 / torch.sqrt((x.double() ** 2).mean(1) + float(np.float32(eps)))
+    dx0, dg0, _, size, dgs, _ = _norm_backward_ref(dy, x, g, None, r, K)
+    # r near the bottom of fp32 is off by half its last place, 2^-150, once in xh and once in front; a result there by
+    # half of bf16's, 2^-134
+    tiny = 2.0 ** -150 / r[:, None]
+    _close(dx, dx0, HALF * dx0.abs() * (1 + HALF) + (256 * U + 3 * tiny) * size + 2.0 ** -134, "dx")
+    _close(dg, dg0, ((M + 300) * U + float(tiny.max())) * dgs, "dg")
+    for got, want in zip(bl.rmsnorm_backward(_strided(dy, 3, 1), _strided(x, 5, 1), g, eps), (dx, dg)):
+        assert torch.equal(got, want)
+    # ordinary rows give the bits that they give alone
+    keep = torch.tensor([i for i in range(M) if i not in far], device=DEV)
+    assert torch.equal(dx[keep], bl.rmsnorm_backward(dy[keep], x[keep], g, eps)[0])
