@@ -419,7 +419,7 @@ bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w, const uin
 #define BITLINEAR_FLAG_ACCUMULATE 0x40u /* bitlinear_backward_weight: add to dW instead of writing it */
 
 /* Layer norm.  Per row: s1 = sum x, s2 = sum x^2 in fp64; mean = RN32(s1 / K);
- * var = RN32(max(0, (s2 - s1^2 / K) / K)); rstd = RN32(1 / sqrt(var + eps)) (all in
+ * var = RN32(max(0, (K s2 - s1^2) / K^2)); rstd = RN32(1 / sqrt(var + eps)) (all in
  * fp64 before their one rounding); xn = RN32(RN32(RN32(x - mean) * rstd) * w), then
  * RN32(xn + b) with a bias; y = bf16 of xn.
  * x        device, bf16 bits [M, ldx];  w, b  device, fp32 [K] (b may be NULL).

@@ -50,6 +50,7 @@ template <bool kCodes>
 bitlinear_status layernorm_launch(LnArgs a, cudaStream_t s, int sm_count) {
   const int wpr = row_warps(a.M, a.K, kLnMaxChunks, sm_count);
   a.lw = log2i(wpr);
+  a.dk = a.K;
   a.inv_k = 1.0 / a.K;
   const bool fast = rows16(a.x, a.ldx, a.K) && aligned32(a.w) && aligned32(a.b) && aligned16(a.y) && aligned8(a.q);
   const int need = row_chunks(a.K, wpr);

@@ -222,12 +222,13 @@ __device__ __forceinline__ uint2 codes8_exact(const float2 (&v)[4], float d) {
 }
 
 // ----------------------------------------------------------------- layer norm
-// Per row: s1 = sum x, s2 = sum x^2 in fp64 (the squares of bf16 values are
-// exact there, so the one-pass variance s2 - s1^2 / K loses nothing a two-pass
-// one would keep: 53 bits against the 24 of its result even at a mean of a
-// thousand deviations); mean = RN32(s1 / K), var = RN32(max(0, (s2 - s1^2 / K) /
-// K)), rstd = RN32(1 / sqrt(var + eps)), each computed in fp64 (1 / K rounded
-// there once, so that no quotient stands in a row's way), and
+// Per row: s1 = sum x, s2 = sum x^2 in fp64; mean = RN32(s1 / K), var = RN32(max(0, (K s2 - s1^2) / K^2)), rstd = RN32(1 /
+// sqrt(var + eps)), each computed in fp64 (1 / K rounded there once, so that no quotient stands in a row's way).  The
+// one-pass variance loses nothing that a two-pass one would keep: if all entries lie within a factor of two of each
+// other, they are multiples of one 2^e below 2^9 of it, and with K <= 2^16 both K s2 and s1^2 are whole numbers below
+// 2^53 of 4^e, their difference exact (0 for a constant row; s2 - s1^2 / K, with its rounded quotient, gave rows of 1e6
+// a variance of up to 5e-5 and rows of 1e30 an infinite one); otherwise the two are 2^-19 apart or more, which leaves
+// 34 of 53 bits.  Then
 //   xn = RN(RN(RN(x - mean) * rstd) * w) (+ RN b)
 // every operation one fp32 rounding, so that the codes are defined to the bit.
 struct LnArgs {
@@ -244,6 +245,7 @@ struct LnArgs {
   float* mean;     // or null
   float* rstd;     // or null
   int lw;          // log2 of the warps per row
+  double dk;       // K
   double inv_k;    // 1 / K
 };
 
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) la
     }
   }
   const float mean = __double2float_rn(s1 * a.inv_k);
-  const double vard = (s2 - s1 * s1 * a.inv_k) * a.inv_k;
+  const double vard = (a.dk * s2 - s1 * s1) * a.inv_k * a.inv_k;
   const float var = __double2float_rn(vard < 0.0 ? 0.0 : vard);  // NaN stays NaN
   const float rstd = __double2float_rn(rsqrt(static_cast<double>(var) + static_cast<double>(a.eps)));
   if (active && sub == 0 && lane == 0) {

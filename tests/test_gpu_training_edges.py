@@ -53,3 +53,37 @@ def test_rmsnorm_backward_far_rows(K, eps):
     # ordinary rows give the bits that they give alone
     keep = torch.tensor([i for i in range(M) if i not in far], device=DEV)
     assert torch.equal(dx[keep], bl.rmsnorm_backward(dy[keep], x[keep], g, eps)[0])
+
+
+# ---------------------------------------------------------------- layer norm: rows that are constant, or nearly
+@pytest.mark.parametrize("K", [7, 203, 641, 2560, 2561, 11008, 16384, 65536])
+def test_layernorm_nearly_constant_rows(K):
+    """The variance of rows whose mean is far larger than their deviation, as the definition gives it: exactly 0 where all
+    entries are equal, whatever they are, and to the last places where one entry (the first, the last, one between) is
+    a bf16 step away."""
+    fills = [1e4, -1e6, 3e8, 7.7e15, -1e30, 3e38]
+    rows = []
+    for f in fills:
+        base = torch.full((K,), f, device=DEV).to(BF)
+        for at in (None, 0, K // 2, K - 1):
+            r = base.clone()
+            if at is not None:
+                r[at] = (base[at].float() * (1 + 2.0 ** -6)).to(BF) if f < 1e38 else (base[at].float() * 0.5).to(BF)
+            rows.append(r)
+    x = torch.cat([torch.stack(rows), _rand(K, 3, K)])
+    w, b = torch.rand(K, device=DEV) + 0.5, torch.rand(K, device=DEV)
+    d = x.double()
+    mean64 = d[:, :1] + (d - d[:, :1]).mean(1, keepdim=True)
+    var = ((d - mean64) ** 2).mean(1).float()  # rounded once, as defined (infinite beyond fp32)
+    want = (1.0 / torch.sqrt(var.double() + float(np.float32(1e-5)))).float()
+    for xs in (x, _strided(x, 3, 1)):
+        y, mean, rstd = bl.layernorm(xs, w, b, 1e-5, want_stats=True)
+        q, gamma, _, mean_q, rstd_q = bl.layernorm_quant_act(xs, w, b, 1e-5, want_stats=True)
+        assert torch.equal(mean, mean_q) and torch.equal(rstd, rstd_q)
+        const = torch.arange(0, 4 * len(fills), 4, device=DEV)
+        assert torch.equal(mean[const], x[const, 0].float()) and torch.equal(y[const], b.to(BF).expand(len(fills), K))
+        assert torch.equal(rstd[const], want[const])
+        # var + eps and the root: the sums in 64 bits leave at most the other neighbour of each fp32 rounding
+        _close(rstd, want.double(), 4 * U * want.double(), "rstd")
+        m = mean64[:, 0]
+        _close(mean, m, U * m.abs() * (1 + 1e-6), "mean")
