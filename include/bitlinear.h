@@ -477,7 +477,9 @@ bitlinear_status bitlinear_dequant_act(const int8_t* q, int64_t ldq, const float
  * maxima of g, u and h, each as bitlinear_quant_act would (q_* int8 [M, N],
  * gamma_* fp32 [M], rowsum_h int32 [M] or NULL): those of h feed
  * bitlinear_forward_q8 of the down projection and bitlinear_backward_weight,
- * those of g and u bitlinear_relu2_glu_backward.  h itself is not written.
+ * those of g and u bitlinear_relu2_glu_backward.  h itself is not written.  A
+ * NaN of the gate is one of h (of max(g, 0)); a row with a NaN or an infinity has
+ * a row maximum that is NaN or infinite, and codes without meaning.
  * Errors: NULL, SHAPE (also N above BITLINEAR_MAX_K), ALIGN, DEVICE, CUDA. */
 bitlinear_status bitlinear_relu2_glu_quant_act(const uint16_t* g, int64_t ldg, const uint16_t* u, int64_t ldu,
                                                int32_t M, int32_t N, int8_t* q_g, float* gamma_g, int8_t* q_u,
@@ -487,6 +489,7 @@ bitlinear_status bitlinear_relu2_glu_quant_act(const uint16_t* g, int64_t ldg, c
 /* Its backward pass from the checkpoints: with g~, u~ the values of the codes
  * (fp32) and r = max(g~, 0),  dg = 2 dh r u~  and  du = dh r^2, in fp32, each
  * rounded once to bf16.  dh bf16 bits [M, lddh]; dg, du out bf16 bits [M, N].
+ * Rows whose gamma_g is NaN or infinite have gradients of NaN, those whose gamma_u is, a dg of NaN.
  * Errors: NULL, SHAPE, ALIGN, DEVICE, CUDA. */
 bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, const int8_t* q_g,
                                               const float* gamma_g, const int8_t* q_u, const float* gamma_u, int32_t M,

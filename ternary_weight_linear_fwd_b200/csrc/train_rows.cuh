@@ -993,7 +993,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
   auto bits = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); };
   // two of h: each product is exact in more bits than bf16 keeps and is rounded once
   auto hword = [&](uint32_t g, uint32_t u) {
-    const __nv_bfloat162 r = __hmax2(as2(g), as2(0u));  // NaN gives 0, as in the forward pass
+    const __nv_bfloat162 r = __hmax2_nan(as2(g), as2(0u));  // a NaN must reach h and its row's maximum
     return bits(__hmul2_rn(__hmul2_rn(r, r), as2(u)));
   };
   uint32_t mx[3] = {0u, 0u, 0u};  // two maxima of |.| each; NaN is kept
@@ -1085,12 +1085,19 @@ __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 6 ? 3 : 2)
   }
 }
 
+// The step of a row's codes, NaN where the row's maximum is infinite too: such a row's codes are without meaning (most
+// are 0), and max(., 0) would turn some of their products into zero gradients.
+__device__ __forceinline__ float grad_step(float gamma) {
+  const float s = __fdiv_rn(gamma, kQb);
+  return __fadd_rn(s, __fsub_rn(s, s));
+}
+
 // Two of dg = RNb(2 dh r u~) and du = RNb(dh r^2), r = max(g~, 0), of two codes' values g, u each.
 __device__ __forceinline__ void glu_grads2(float2 g, float2 u, uint32_t dh, float2 sg, float2 su, uint32_t& dg,
                                            uint32_t& du) {
   const float2 d = bf16_2(dh);
   float2 rp = __fmul2_rn(g, sg);
-  rp = make_float2(fmaxf(rp.x, 0.0f), fmaxf(rp.y, 0.0f));
+  rp = make_float2(max_nan(rp.x, 0.0f), max_nan(rp.y, 0.0f));
   const float2 dr = __fmul2_rn(d, rp);
   const float2 p = __fmul2_rn(__fadd2_rn(dr, dr), __fmul2_rn(u, su)), q = __fmul2_rn(dr, rp);
   dg = pack_bf16x2(p.x, p.y);
@@ -1133,8 +1140,8 @@ __global__ void __launch_bounds__(256, 4)
     float a[2], b[2];
 #pragma unroll
     for (int r = 0; r < (kSplit ? 2 : 1); ++r) {
-      a[r] = __fdiv_rn(sg[j][r], kQb);
-      b[r] = __fdiv_rn(su[j][r], kQb);
+      a[r] = grad_step(sg[j][r]);
+      b[r] = grad_step(su[j][r]);
     }
     const uint32_t g4[4] = {wg[j].x, wg[j].y, wg[j].z, wg[j].w}, u4[4] = {wu[j].x, wu[j].y, wu[j].z, wu[j].w};
     uint32_t og[8], ou[8];
@@ -1161,7 +1168,7 @@ __global__ void __launch_bounds__(256, 4)
     const uint32_t e = 16 * total + threadIdx.x, row = e / N;
     uint32_t p, q;
     glu_grads2(splat2(static_cast<float>(qg[e])), splat2(static_cast<float>(qu[e])), dh[e],
-               splat2(__fdiv_rn(gg[row], kQb)), splat2(__fdiv_rn(gu[row], kQb)), p, q);
+               splat2(grad_step(gg[row])), splat2(grad_step(gu[row])), p, q);
     dg[e] = static_cast<uint16_t>(p);
     du[e] = static_cast<uint16_t>(q);
   }
@@ -1178,7 +1185,7 @@ __global__ void __launch_bounds__(256) relu2_glu_backward_kernel(
   const int r = threadIdx.x / lanes, t = threadIdx.x - r * lanes;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / lanes) + r;
   if (row >= M) return;
-  const float sg = __fdiv_rn(gg[row], kQb), su = __fdiv_rn(gu[row], kQb);
+  const float sg = grad_step(gg[row]), su = grad_step(gu[row]);
   const uint16_t* const end = dh + static_cast<int64_t>(M - 1) * lddh + N;
   const size_t codes = static_cast<size_t>(M) * N;
   const bool vo = (N % 8) == 0 && ((reinterpret_cast<uintptr_t>(dg) | reinterpret_cast<uintptr_t>(du)) & 15u) == 0;

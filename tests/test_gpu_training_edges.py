@@ -87,3 +87,32 @@ def test_layernorm_nearly_constant_rows(K):
         _close(rstd, want.double(), 4 * U * want.double(), "rstd")
         m = mean64[:, 0]
         _close(mean, m, U * m.abs() * (1 + 1e-6), "mean")
+
+
+# ---------------------------------------------------------------- gated FFN: a NaN or an infinity does not vanish
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("N", [1, 16, 203, 272, 6912])
+@pytest.mark.parametrize("at", [0, -1])
+def test_gate_keeps_what_is_not_a_number(N, at, bad):
+    """A gate row with a NaN or an infinity has no restored values: all its gradients are NaN; a row of u, its dg.  Through
+    max(., 0) the plain form gives the same.  Other rows keep their bits, on every path."""
+    M = 7
+    g, u, dh = _rand(N, M, N), _rand(N + 1, M, N), _rand(N + 2, M, N)
+    clean = bl.relu2_glu_quant_act(g, u)
+    dg0, du0 = bl.relu2_glu_backward(dh, *clean[:4])
+    g2, u2 = g.clone(), u.clone()
+    g2[2, at] = bad
+    u2[4, at] = bad
+    for gs, us, ds in ((g2, u2, dh), (_strided(g2, 3, 1), _strided(u2, 5), _strided(dh, 3, 1))):
+        c = bl.relu2_glu_quant_act(gs, us)
+        assert not bool(torch.isfinite(c.gamma_g[2])) and not bool(torch.isfinite(c.gamma_u[4]))
+        if bad != float("-inf"):  # max(-inf, 0) = 0
+            assert not bool(torch.isfinite(c.gamma_h[2]))
+        assert not bool(torch.isfinite(c.gamma_h[4]))  # r u, or 0 times an infinity
+        dg, du = bl.relu2_glu_backward(ds, *c[:4])
+        assert bool(dg[2].isnan().all()) and bool(du[2].isnan().all()) and bool(dg[4].isnan().all())
+        assert torch.equal(du[4], du0[4])
+        keep = [0, 1, 3, 5, 6]
+        assert torch.equal(dg[keep], dg0[keep]) and torch.equal(du[keep], du0[keep])
+        for got, want in zip(c, clean):
+            assert torch.equal(got[keep], want[keep])
