@@ -13,8 +13,6 @@ import os
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
-import torch
-
 __all__ = [
     "BitLinearError", "PackedWeights", "lib", "packed_layout", "pack_weights", "pack_ternary",
     "quant_act", "rmsnorm_quant_act", "forward", "forward_nm", "forward_group", "forward_norm",
@@ -428,11 +426,19 @@ class _Here:
 
 
 _HERE_CTX = _Here()
-_BF16, _F32, _I8, _I32 = torch.bfloat16, torch.float32, torch.int8, torch.int32
+torch = _BF16 = _F32 = _I8 = _I32 = None  # bound by the first training call: sizes and layouts need no torch
+
+
+def _bind_torch():
+    global torch, _BF16, _F32, _I8, _I32
+    import torch
+    _BF16, _F32, _I8, _I32 = torch.bfloat16, torch.float32, torch.int8, torch.int32
 
 
 def _on(device, stream):
     """Context in which a call's outputs and workspace are allocated and its kernels are launched."""
+    if torch is None:
+        _bind_torch()
     if stream is None:
         if device.index is not None and device.index == torch._C._cuda_getDevice():
             return _HERE_CTX  # entering torch.cuda.device costs more than a small kernel
