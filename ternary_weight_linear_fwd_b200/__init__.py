@@ -471,6 +471,14 @@ def _mat(t, what: str, dtype, device=None, shape=None, align: int = 1):
     return t, (t.stride(0) if M > 1 else K)
 
 
+def _packed_mat(t, what: str, dtype, device, shape):
+    """The same for a matrix that a kernel reads contiguous: row-strided views are copied too."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t
+    t, ld = _mat(t, what, dtype, device, shape)
+    return t if ld == shape[1] else t.contiguous()
+
+
 def _new(like, dtype=None):
     """An uninitialised contiguous tensor of the same shape and device."""
     return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
@@ -620,8 +628,8 @@ def relu2_glu_backward(dh, q_g, gamma_g, q_u, gamma_u, stream=None):
     with _on(dh.device, stream):
         dh, lddh = _mat(dh, "dh", _BF16)
         M, N = dh.shape
-        _check_out(q_g, (M, N), _I8, dh.device, "q_g")
-        _check_out(q_u, (M, N), _I8, dh.device, "q_u")
+        q_g = _packed_mat(q_g, "q_g", _I8, dh.device, (M, N))
+        q_u = _packed_mat(q_u, "q_u", _I8, dh.device, (M, N))
         gamma_g, gamma_u = _vec(gamma_g, "gamma_g", M, dh.device), _vec(gamma_u, "gamma_u", M, dh.device)
         dg, du = _new(dh), _new(dh)
         _check(lib().bitlinear_relu2_glu_backward(_ptr(dh), lddh, _ptr(q_g), _ptr(gamma_g), _ptr(q_u), _ptr(gamma_u),
@@ -677,7 +685,7 @@ def backward_input(w: PackedWeights, dy, add=None, out=None, workspace=None, str
         if w.codes.device != dy.device:
             raise ValueError(f"backward_input: weights on {w.codes.device}, dy on {dy.device}")
         if add is not None:
-            _check_out(add, (M, w.K), _BF16, dy.device, "add")
+            add = _packed_mat(add, "add", _BF16, dy.device, (M, w.K))
         if out is not None:
             _check_out(out, (M, w.K), _BF16, dy.device, "out")
         dx = out if out is not None else dy.new_empty((M, w.K))

@@ -116,3 +116,32 @@ def test_gate_keeps_what_is_not_a_number(N, at, bad):
         assert torch.equal(dg[keep], dg0[keep]) and torch.equal(du[keep], du0[keep])
         for got, want in zip(c, clean):
             assert torch.equal(got[keep], want[keep])
+
+
+# ---------------------------------------------------------------- row-strided views wherever a matrix is read
+@pytest.mark.parametrize("M", [1, 21])
+@pytest.mark.parametrize("pad,off", [(16, 0), (3, 0), (0, 1)])
+def test_strided_codes_and_addend(M, pad, off):
+    """The codes that relu2_glu_backward reads and the gradient that backward_input adds, as slices of wider matrices,
+    with their columns apart, or expanded."""
+    N, K = 272, 200
+    c = bl.relu2_glu_quant_act(_rand(1, M, N), _rand(2, M, N))
+    dh = _rand(3, M, N, scale=1e-3)
+    want = bl.relu2_glu_backward(dh, *c[:4])
+    both = torch.cat([c.q_g, c.q_u], 1)
+    for q_g, q_u in ((_strided(c.q_g, pad, off), _strided(c.q_u, pad + 5, off)), (both[:, :N], both[:, N:]),
+                     (c.q_g.t().contiguous().t(), c.q_u.t().contiguous().t())):
+        for got, ref in zip(bl.relu2_glu_backward(dh, q_g, c.gamma_g, q_u, c.gamma_u), want):
+            assert torch.equal(got, ref)
+    w = bl.pack_ternary(torch.randint(-1, 2, (N, K), device=DEV, generator=_gen(3), dtype=torch.int8), 0.02)
+    add = _rand(4, M, K)
+    ref = bl.backward_input(w, dh, add=add)
+    assert torch.equal(bl.backward_input(w, dh, add=_strided(add, pad, off)), ref)
+    one = torch.full((1, 1), 0.25, dtype=BF, device=DEV).expand(M, K)
+    assert torch.equal(bl.backward_input(w, dh, add=one), bl.backward_input(w, dh, add=one.contiguous()))
+    for bad in (add[:, :-1], add.float(), add.cpu(), add.view(-1)):
+        with pytest.raises(ValueError):
+            bl.backward_input(w, dh, add=bad)
+    for bad in (c.q_g[:, :-1], c.q_g.int(), c.q_g.cpu(), c.q_g.view(-1)):
+        with pytest.raises(ValueError):
+            bl.relu2_glu_backward(dh, bad, c.gamma_g, c.q_u, c.gamma_u)
