@@ -217,9 +217,8 @@ GgPlan bw_plan(int N, int K, int M, int sm_count) {
   return gg_plan(N, K, M, M > kGgOneSum * kGgRed ? 0.38 : 0.53, sm_count);
 }
 
-size_t gg_slab_bytes(const GgPlan& p) {
-  return static_cast<size_t>(p.units - p.full) * kGgSlab * 4;
-}
+size_t gg_slab_bytes(const GgPlan& p) { return static_cast<size_t>(p.units - p.full) * kGgSlab * 4; }
+size_t gg_done_bytes(const GgPlan& p) { return static_cast<size_t>(p.units - p.full) * 2 * kGgStoring * 4; }
 
 // Whether a product restores its compressed operand (`elems` elements) to bf16 before it starts: where what its
 // k-blocks save (us each, against expanding in place) exceeds the extra pass, a launch and `bytes` of traffic an
@@ -249,14 +248,14 @@ bitlinear_status few_launch(FewArgs a, cudaStream_t s, int sm_count) {
   return launch_ex(few_input_kernel, dim3(groups * a.cs, mt), dim3(32 * kFewWarps), kFewSmem, s, true, a.cs, a);
 }
 
-// Workspace: slabs | dy with padded rows | B: codes with padded rows, expanded N:M codes, or bf16 values.
+// Workspace: slabs and their marks | dy with padded rows | B: codes with padded rows, expanded N:M codes, or bf16 values.
 struct GgLayout {
   size_t dy, b, total;  // offsets of the second and third part, whole size
   int64_t lddy;         // row stride of dy that TMA reads, in elements
 };
 GgLayout gg_layout(const GgPlan& p, int64_t M, int64_t N, int64_t lddy, size_t b_bytes) {
   GgLayout l;
-  l.dy = align256(gg_slab_bytes(p));
+  l.dy = align256(gg_slab_bytes(p) + gg_done_bytes(p));
   const bool pad = lddy % 8 != 0;
   l.lddy = pad ? (N + 7) / 8 * 8 : lddy;
   l.b = l.dy + (pad ? align256(static_cast<size_t>(M) * l.lddy * 2) : 0);
@@ -353,6 +352,7 @@ void gg_args(GradArgs* a, const GgPlan& p, int rows, int cols, int red, void* ws
   a->split = p.split;
   a->per = p.per;
   a->slab = static_cast<float*>(ws);
+  a->done = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + gg_slab_bytes(p));
   a->status = dev->status;
 }
 

@@ -79,6 +79,7 @@ struct GradArgs {
   int vec;                // output (and add) rows are 32-byte aligned
   int tma;                // dW: stored (or added) by TMA
   float* slab;            // [(tiles - full) * split][32 groups of 8 columns][256 rows][8]: a warp's store is contiguous
+  uint32_t* done;         // [(tiles - full) * split][2 CTAs][kGgStoring]: 1 where the warp stored its share of the part
   int32_t* status;
 };
 
@@ -225,6 +226,12 @@ __device__ __forceinline__ void grad_store_tile(const GradArgs& a, int64_t row0,
   }
 }
 
+// The mark of a storing warp's share of part g - a.full (none for tiles that are not split): every warp of every launch
+// writes its marks, 0 for what it gave up on, so that grad_reduce_kernel adds up no slab that an earlier call left.
+__device__ __forceinline__ void grad_mark(const GradArgs& a, int g, uint32_t rank, int sw, uint32_t v) {
+  if (g >= a.full && a.split > 1) a.done[static_cast<size_t>(g - a.full) * (2 * kGgStoring) + rank * kGgStoring + sw] = v;
+}
+
 // mapA: dy; box 128 bytes x 128 rows (dx) or 128 bytes x 64 rows (dW), landed 128-byte-swizzled.
 // mapB: the compressed rows; box 32 bytes (2-bit) or 128 bytes (8-bit) x 64 rows, landed as they are; with kDense the
 // bf16 rows, box 128 bytes x 64 rows, landed 128-byte-swizzled.  mapC (dW, a.tma): fp32, box 32 x 32, 128-byte-swizzled.
@@ -238,6 +245,10 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
   // both CTAs see the same offset, so both leave here together (before any cluster barrier)
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
     if (threadIdx.x == 0) *a.status = kDevBadSmemAlign;
+    pdl_wait_primary();
+    if (threadIdx.x < kGgStoring)
+      for (int g = blockIdx.x >> 1; g < a.units; g += gridDim.x >> 1)
+        grad_mark(a, g, cluster_ctarank(), static_cast<int>(threadIdx.x), 0u);
     return;
   }
   uint8_t* sA = smem_raw;                   // [S][16 KB]
@@ -469,13 +480,14 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
     }
   } else if (warp >= 4 + 4 * G) {
     // -------------------------------------------------------------- stores (both CTAs, own rows)
-    const int q = warp & 3, first = ((warp - 4 - 4 * G) >> 2) * 32;  // 32 rows, every other 32 columns
+    const int sw = warp - 4 - 4 * G;
+    const int q = sw & 3, first = (sw >> 2) * 32;  // 32 rows, every other 32 columns
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float alpha = kWeight ? 1.0f : *a.alpha;
     // 32 columns of a row a lane, from c0 of the tile: to their slab, or finished
     auto finish = [&](int g, int row0, int col0, int wrow, int c0, const float (&v)[32], const uint32_t (&s0)[16]) {
       const bool part = g >= a.full && a.split > 1;
-      float* out = sOut + (warp - 4 - 4 * G) * 1024;
+      float* out = sOut + sw * 1024;
       if (row0 + wrow < a.rows && col0 + c0 < a.cols) {
         if (part) {
           float* p = a.slab + static_cast<size_t>(g - a.full) * kGgSlab + (c0 / 8 * kGgRows + wrow + lane) * 8;
@@ -505,8 +517,8 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
         }
       }
     };
-    int t = 0;
-    for (int g = pair; g < a.units; g += npairs) {
+    int t = 0, g = pair;
+    for (; g < a.units; g += npairs) {
       int row0, col0, kb0;
       const int n = unit_of(g, row0, col0, kb0);
       const int wrow = static_cast<int>(rank) * 128 + q * 32;  // the warp's first row of the tile
@@ -574,7 +586,10 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
         if (lane == 0) mbar_arrive_remote_cta(accempty0 + static_cast<uint32_t>(buf * 8));
         ++t;
       }
+      if (lane == 0) grad_mark(a, g, rank, sw, 1u);
     }
+    for (; g < a.units; g += npairs)  // given up
+      if (lane == 0) grad_mark(a, g, rank, sw, 0u);
     if (kWeight && lane == 0) bulk_wait_read<0>();  // the stores have read the tiles before the CTA ends
   }
   tc_fence_before();
@@ -587,8 +602,9 @@ __global__ void __launch_bounds__(GG<kWeight, kDense>::THREADS, 1)
   }
 }
 
-// The split tiles: adds each tile's parts in order and finishes it.  A thread
-// takes 16 columns of a row, four parts' loads in flight.
+// The split tiles: adds each tile's parts in order and finishes it, but for what
+// has a part that was given up on.  A thread takes 16 columns of a row, four
+// parts' loads in flight.
 constexpr int kGgReduceCtas = kGgRows * kGgCols / 16 / 256;  // of a tile
 template <bool kWeight>
 __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
@@ -604,18 +620,22 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradArgs a) {
   const float* p = a.slab + static_cast<size_t>(unit) * a.split * kGgSlab + (lc / 8 * kGgRows + lrow) * 8;
   uint32_t add[kWeight ? 16 : 8];
   grad_addend<kWeight, 16>(a, row, col, add);
+  const uint32_t* done = a.done + static_cast<size_t>(unit) * a.split * (2 * kGgStoring) + (lrow >> 7) * kGgStoring +
+                         ((lc >> 5) & 1) * 4 + ((lrow >> 5) & 3);  // of the warp that stored these
+  uint32_t all = 1u;
   float v[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) v[c] = 0.0f;
 #pragma unroll 4
   for (int s = 0; s < a.split; ++s) {
+    all &= done[s * (2 * kGgStoring)];
     uint32_t w[16];
     ld_global_v8(p + static_cast<size_t>(s) * kGgSlab, w);
     ld_global_v8(p + static_cast<size_t>(s) * kGgSlab + 8 * kGgRows, w + 8);
 #pragma unroll
     for (int c = 0; c < 16; ++c) v[c] = __fadd_rn(v[c], __uint_as_float(w[c]));
   }
-  grad_store<kWeight, 16>(a, row, col, v, add, kWeight ? 1.0f : *a.alpha);
+  if (all) grad_store<kWeight, 16>(a, row, col, v, add, kWeight ? 1.0f : *a.alpha);
 }
 
 // ----------------------------------------------------------------- operands put in order
