@@ -496,10 +496,13 @@ bitlinear_status bitlinear_relu2_glu_backward(const uint16_t* dh, int64_t lddh, 
                                               int32_t N, uint16_t* dg, uint16_t* du, void* stream);
 
 /* dW = dy^T x~: the gradient of a BitLinear's latent weights from the 8-bit
- * checkpoint of its input, x~ restored in bf16 (bitlinear_dequant_act), the
- * products exact and the sums in fp32 (pieces of at most 896 tokens on the tensor
- * cores, which cut off below the last place, then rounded additions: together
- * within about 1e-6 of the sum of the terms' magnitudes).  For N:M weights this is the gradient
+ * checkpoint of its input, x~ restored in bf16 (bitlinear_dequant_act; the
+ * forward pass multiplies with the unrounded value, at most 2^-8 of it away),
+ * the products exact and the sums in fp32: pieces of at most 896 tokens on the
+ * tensor cores, which cut off below the last place, then rounded additions.
+ * Against the exact sum of these products, at any number of tokens: within 1e-6 of
+ * the result's norm with terms of both signs, within 3e-6 of the sum of the
+ * magnitudes where all terms have one.  For N:M weights this is the gradient
  * of every latent weight, kept or not (the "dual" estimator of the
  * Sparse-BitNet review, section 3.3).
  * dy       device, bf16 bits [M, lddy] (N used);  q  device, int8 [M, ldq] (K

@@ -56,11 +56,14 @@ constexpr int kGgCols = 256;      // columns of a pair tile (128 of B a CTA)
 constexpr int kGgRed = 64;        // steps of the reduction per stage
 constexpr int kGgStoring = 8;      // storing warps, two for each 32 rows: one waits for memory while the other computes
 constexpr int kGgGroups = 2;       // groups of four expanding warps, taking the stages in turn
-// dW: k-blocks (12: 768 tokens) that are summed in TMEM.  The tensor cores cut every addition off below its last place,
-// always towards zero, so the error of a sum grows with its length (relative, 777 tokens 6e-7, 2048 1.7e-6, 8192 7e-6);
-// longer reductions are added up from pieces of this length in registers, rounded to nearest (7e-7 at any length).
+// dW: k-blocks that are summed in TMEM.  The tensor cores cut every addition off below its last place, always towards
+// zero, so the error of a sum grows with its length: of a 512 x 9472 result's norm (terms of both signs) 2.1e-7 with 4
+// k-blocks, 4.5e-7 with 8, 6.9e-7 with 12, 7.4e-7 with 13, 8.1e-7 with 14, 8.9e-7 with 15, 1.5e-6 with 24, 8.9e-6 with 128.
+// Allowed is less than the fp32 library product has at 8192 tokens, 8.9e-7: one sum may have 14 k-blocks (896 tokens).
+// Longer ones are added up from pieces in registers, rounded to nearest, whose length leaves room for that: of 12, 6.3e-7
+// to 6.9e-7 at any number of tokens.  (Terms of one sign: 2.7e-6 of the sum with one of 14, 2.0e-6 with pieces of 12.)
 constexpr int kGgChunk = 12;
-constexpr int kGgOneSum = 14;  // reductions up to this long (896 tokens, 8e-7) may stay one sum: the kernel with expansion
+constexpr int kGgOneSum = 14;  // up to here the kernel with expansion, which has no registers to add up pieces
 constexpr int kGgSlab = kGgRows * kGgCols;  // fp32 of one part of a split tile
 
 struct GradArgs {
