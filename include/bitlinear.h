@@ -405,7 +405,11 @@ bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w, const uin
  *
  * Value of a code: v = RN32(q * RN32(gamma / 127)); restored as an activation
  * (bitlinear_dequant_act, and the x~ of bitlinear_backward_weight) it is
- * rounded once more, to bf16, the type the activation had.
+ * rounded once more, to bf16, the type the activation had.  The codes were made
+ * with gamma + 1e-5, so the values of a row whose maximum is not far above that
+ * come out low: by 1% at gamma = 1e-3, by 9% at 1e-4.  For x and h that is what
+ * the forward product multiplies with; the gated FFN's backward pass computes its
+ * gradients at these values of g and u, the forward pass h from g and u themselves.
  *
  * Rows may be strided: ld* counts elements between rows and is at least the
  * row's length.  Matrices whose ld is a multiple of 8 (bf16) or 16 (codes) and
@@ -423,7 +427,8 @@ bitlinear_status bitlinear_forward_noalloc(const bitlinear_weights* w, const uin
  * fp64 before their one rounding); xn = RN32(RN32(RN32(x - mean) * rstd) * w), then
  * RN32(xn + b) with a bias; y = bf16 of xn.
  * x        device, bf16 bits [M, ldx];  w, b  device, fp32 [K] (b may be NULL).
- * eps      0 <= eps <= 1 (with eps = 0 a constant row is undefined).
+ * eps      0 <= eps <= 1 (with eps = 0 a constant row is undefined).  Rows whose
+ *          variance passes fp32's range (deviations beyond 1.8e19) get rstd = 0.
  * y        device, out: bf16 bits [M, K].
  * mean, rstd  device, out (may be NULL): fp32 [M], for the backward pass.
  * Errors: NULL, SHAPE (also ldx < K, eps out of range), ALIGN, DEVICE, CUDA. */
@@ -521,8 +526,9 @@ bitlinear_status bitlinear_backward_weight(const uint16_t* dy, int64_t lddy, con
 
 /* dx = alpha dy W_t (+ add): the gradient of a BitLinear's input, the products
  * exact, the sums in fp32 (on the tensor cores, which cut off below the last
- * place: about 1e-9 of the sum a term, less than the rounding to bf16 up to N =
- * 2^20), one rounding to bf16 at the end.  add is the
+ * place: about 1e-9 of the result's norm a term with terms of both signs, 4e-9 of
+ * the sum where all have one, less than the rounding to bf16 up to N = 2^19), one
+ * rounding to bf16 at the end.  add is the
  * gradient that reaches the same input another way (the up projection's beside
  * the gate's, or the residual path's).
  * w        dense or N:M weights.

@@ -3,8 +3,11 @@
 // passes of layer norm and RMSNorm, the 8-bit checkpoint of the squared-ReLU
 // gated FFN with the backward pass that reads it, and the restored activation.
 //
-// All of them are bound by memory: a few operations per element, every input
-// read once and every output written once.
+// Every input is read once and every output written once, with a few operations
+// per element.  What bounds them: memory for the restored activation and the
+// gate's gradients (the copy rate at 4096 x 11008), latency between a row's
+// passes for the layer norm, instructions for the codes of three matrices and
+// for the norm gradients, both near half of the issue slots.
 #pragma once
 #include "gemv.cuh"
 
@@ -137,19 +140,14 @@ __device__ __forceinline__ void store8_codes(int8_t* row, int k0, int K, bool ve
   }
 }
 
-// 16 codes from row[k0 ..] (zero past K).
-__device__ __forceinline__ void load16_codes(const int8_t* row, int k0, int K, bool vec, uint32_t (&w)[4]) {
-  if (vec && k0 + 16 <= K) {
-    const uint4 t = *reinterpret_cast<const uint4*>(row + k0);
-    w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
-  } else {
+// 16 codes from row[k0 ..] (zero past K), one by one.
+__device__ __forceinline__ void load16_codes(const int8_t* row, int k0, int K, uint32_t (&w)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = 0u;
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (k0 + 4 * i + j < K) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k0 + 4 * i + j])) << (8 * j);
-    }
+    for (int j = 0; j < 4; ++j)
+      if (k0 + 4 * i + j < K) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k0 + 4 * i + j])) << (8 * j);
   }
 }
 
@@ -160,7 +158,7 @@ __device__ __forceinline__ void load16_codes_any(const int8_t* row, int k0, int 
   const uint32_t s = static_cast<uint32_t>(p & 15u);
   const uintptr_t b = s ? a + 16 : a;
   if (k0 + 16 > K || a < reinterpret_cast<uintptr_t>(lo) || b + 16 > reinterpret_cast<uintptr_t>(hi)) {
-    load16_codes(row, k0, K, false, r);
+    load16_codes(row, k0, K, r);
     return;
   }
   const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
@@ -255,8 +253,9 @@ struct LnArgs {
 // normalised values stay in registers between the maximum and the rounding, so
 // the parameters are read once a row as well (read twice, 16 columns a lane,
 // they filled the L1 pipe for 42 us at 4096 x 2560).  Without kAny (rows and
-// parameters that 16- and 32-byte loads can take, K % 8 == 0) the (chunks past K read the last one and are left out
-// of sums, maximum and output), so that those of several go out together.
+// parameters that 16- and 32-byte loads can take, K % 8 == 0) no load is
+// conditional, so that those of several chunks go out together: chunks past K
+// read the last one and are left out of sums, maximum and output.
 // G = 0: rows longer than any G holds are read again for each pass, from L2.
 template <bool kCodes, bool kAny, int G>
 __global__ void __launch_bounds__(32 * kQuantWarps, G >= 1 && G <= 4 ? 3 : 2) layernorm_kernel(const LnArgs a) {
@@ -869,11 +868,10 @@ __global__ void __launch_bounds__(256) dequant_act_kernel(const int8_t* __restri
 // The element-wise kernels for contiguous matrices of at least 16 columns (the
 // matrix as one row of `count` elements): chunks of 16 are dealt to threads
 // regardless of the rows, of which a chunk meets at most two, and each thread's
-// loads go out together.  The kernels above and below, for rows that are apart,
-// wait for one chunk before they ask for the next (latency took three quarters
-// of their time: 7.8 us for 2048 x 2560 restored values, 22.9 for the gate's
-// gradients at 2048 x 6912).  What is left of the last chunk goes element by
-// element.
+// loads go out together: 5.5 us for 4096 x 2560 restored values, 9.6 for the
+// gate's gradients there.  The two kernels for rows that are apart wait for one
+// chunk before they ask for the next (8.8 and 16.8; latency takes three quarters
+// of their time).  What is left of the last chunk goes element by element.
 struct FlatChunk {
   uint32_t row;   // of its first element
   uint32_t left;  // elements of the chunk in that row

@@ -145,3 +145,26 @@ def test_strided_codes_and_addend(M, pad, off):
     for bad in (c.q_g[:, :-1], c.q_g.int(), c.q_g.cpu(), c.q_g.view(-1)):
         with pytest.raises(ValueError):
             bl.relu2_glu_backward(dh, bad, c.gamma_g, c.q_u, c.gamma_u)
+
+
+# ---------------------------------------------------------------- rows hardly above the codes' 1e-5
+def test_small_rows_restored_as_documented():
+    """Codes are made with gamma + 1e-5 and stand for q gamma / 127: low by 1% at a maximum of 1e-3, 9% at 1e-4, half at
+    1e-5, to within half a step of the codes."""
+    tops = [1.0, 1e-2, 1e-3, 1e-4, 1e-5, 1e-7]
+    N = 640
+    x = torch.randn(len(tops), N, device=DEV, generator=_gen(1)).clamp(-1, 1)
+    x[:, 0] = 1.0
+    x = (x * torch.tensor(tops, device=DEV)[:, None]).to(BF)
+    q, gamma, _ = bl.quant_act(x)
+    c = bl.relu2_glu_quant_act(x, x)
+    assert torch.equal(c.q_g, q) and torch.equal(c.gamma_u, gamma)
+    g = gamma.double()[:, None]
+    low = g / (g + 1e-5)
+    # half a step of the codes, and the bf16 rounding
+    _close(bl.dequant_act(q, gamma), x.double() * low, (0.5 + 1e-3) * g / 127 + HALF * x.double().abs() + 1e-38, "restored")
+    dh = torch.ones_like(x)
+    dg, du = bl.relu2_glu_backward(dh, *c[:4])
+    v = (q.double() * (g / 127)).clamp_min(0)
+    _close(du, v * v, (HALF * (1 + HALF) + 6 * U) * v * v + 1e-38, "du")
+    _close(dg, 2 * v * v, (HALF * (1 + HALF) + 6 * U) * 2 * v * v + 1e-38, "dg")
