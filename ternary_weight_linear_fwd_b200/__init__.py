@@ -414,6 +414,7 @@ def forward_norm(w: PackedWeights, x, g, eps: float, want_acc: bool = False, fla
 # Matrices may be row-strided views (unit stride inside a row); anything else is copied first.  All tensors of
 # a call are on one device, which need not be the current one; work goes to `stream` or that device's current
 # stream, and what the call allocates belongs to the stream it runs on.
+# `out` may not overlap what the call reads.
 
 class _Here:
     """The empty context, for calls on the current device and stream."""
